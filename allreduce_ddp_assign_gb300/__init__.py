@@ -25,6 +25,8 @@ DDP_ORDER_REVERSE, DDP_ORDER_FWD_THEN_REVERSE, DDP_ORDER_MEGATRON = 0, 1, 2
 DDP_ALLREDUCE, DDP_REDUCE_SCATTER = 0, 1
 DDP_R_FUSED, DDP_R_COPY_BACK, DDP_R_TIMING, DDP_R_DRY_RUN, DDP_R_COALESCE = 1, 2, 4, 8, 16
 DDP_R_WIRE_BF16, DDP_R_WIRE_F16, DDP_R_BUCKET_DONE = 32, 64, 128
+DDP_NORM_L2, DDP_NORM_INF = 0, 1
+DDP_CLIP_WORKSPACE_BYTES = 65536
 DDP_KERNEL_AUTO, DDP_KERNEL_PLAIN, DDP_KERNEL_STREAM, DDP_KERNEL_STREAM_DYNAMIC = 0, 1, 2, 3
 
 
@@ -111,6 +113,22 @@ _SIGS = {
     "ddp_reducer_create_from_plan": (C.c_int32, [_vp, C.POINTER(BucketDesc), C.c_int32, C.c_int32, C.c_int32, _vp, _vp,
                                                  C.c_int32, _vp, _vp, _vp, _vp, C.POINTER(_vp)]),
     "ddp_plan_destroy": (None, [_vp]),
+    "ddp_grad_norm": (C.c_int32, [_vp, _vp, _vp, C.c_int32, C.c_int64, C.c_int32, _vp, _vp, C.c_int64, _vp]),
+    "ddp_clip_grads": (C.c_int32, [_vp, _vp, _vp, _vp, C.c_int32, C.c_int64, C.c_int32, C.c_float, _vp, _vp, C.c_int64,
+                                   _vp]),
+    "ddp_embedding_forward": (C.c_int32, [_vp, C.c_int64, C.c_int32, C.c_int64, C.c_int64, _vp, C.c_int32, C.c_int64,
+                                          C.c_float, _vp, C.c_int64, _vp]),
+    "ddp_embedding_workspace": (C.c_int32, [C.c_int64, C.c_int64, C.c_int64, _i64p]),
+    "ddp_embedding_backward": (C.c_int32, [_vp, C.c_int64, C.c_int32, _vp, C.c_int32, C.c_int64, C.c_float, C.c_int64,
+                                           C.c_int64, C.c_int64, _vp, C.c_int64, C.c_int32, C.c_int32, _vp, C.c_int64,
+                                           _vp]),
+    "ddp_vocab_loss_workspace": (C.c_int32, [C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int32, _i64p, _i64p]),
+    "ddp_vocab_loss_forward": (C.c_int32, [_vp, C.c_int64, _vp, C.c_int64, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                                           _vp, C.c_int32, C.c_int64, _vp, _vp, _vp, C.c_int64, _vp]),
+    "ddp_vocab_loss_backward": (C.c_int32, [_vp, C.c_int64, _vp, C.c_int64, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                                            _vp, C.c_int32, C.c_int64, _vp, _vp, C.c_int32, _vp, C.c_int64, _vp,
+                                            C.c_int64, C.c_int32, C.c_int32, C.c_int64, _vp, C.c_int64, _vp]),
+    "ddp_lm_status": (C.c_int32, [_vp, _i32p, C.c_int32]),
     "ddp_status_str": (C.c_char_p, [C.c_int32]),
     "ddp_last_error_message": (C.c_char_p, []),
     "ddp_version": (C.c_int32, []),
@@ -533,6 +551,72 @@ def ddp_reducer_bucket_ms(r, nbuckets) -> np.ndarray:
 def ddp_reducer_destroy(r) -> None:
     if r:
         lib().ddp_reducer_destroy(r)
+
+
+# ---------------------------------------------------------------------------
+# language-model ends: clipping, token embedding, vocabulary loss
+# ---------------------------------------------------------------------------
+def ddp_grad_norm(grads, offset, dtypes, ntensors, total, norm_type, norm, workspace, workspace_bytes,
+                  stream=None) -> None:
+    _check(lib().ddp_grad_norm(_ptr(grads), _ptr(offset), _ptr(dtypes), ntensors, total, norm_type, _ptr(norm),
+                               _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ddp_clip_grads(grads, out, offset, dtypes, ntensors, total, norm_type, max_norm, norm, workspace, workspace_bytes,
+                   stream=None) -> None:
+    _check(lib().ddp_clip_grads(_ptr(grads), _ptr(out), _ptr(offset), _ptr(dtypes), ntensors, total, norm_type,
+                                max_norm, _ptr(norm), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ddp_embedding_forward(weight, weight_stride, dtype, vocab, dim, ids, id_bytes, ntokens, scale, out, out_stride,
+                          stream=None) -> None:
+    _check(lib().ddp_embedding_forward(_ptr(weight), weight_stride, dtype, vocab, dim, _ptr(ids), id_bytes, ntokens,
+                                       scale, _ptr(out), out_stride, _stream(stream)))
+
+
+def ddp_embedding_workspace(ntokens, vocab, dim) -> int:
+    b = C.c_int64(0)
+    _check(lib().ddp_embedding_workspace(ntokens, vocab, dim, C.byref(b)))
+    return b.value
+
+
+def ddp_embedding_backward(grad_out, grad_stride, dtype, ids, id_bytes, ntokens, scale, padding_idx, vocab, dim,
+                           grad_weight, gw_stride, gw_dtype, accumulate, workspace, workspace_bytes,
+                           stream=None) -> None:
+    _check(lib().ddp_embedding_backward(_ptr(grad_out), grad_stride, dtype, _ptr(ids), id_bytes, ntokens, scale,
+                                        padding_idx, vocab, dim, _ptr(grad_weight), gw_stride, gw_dtype,
+                                        int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ddp_vocab_loss_workspace(ntokens, vocab, dim, piece=0, weight_aligned=1) -> tuple:
+    """(forward bytes, backward bytes)"""
+    f, b = C.c_int64(0), C.c_int64(0)
+    _check(lib().ddp_vocab_loss_workspace(ntokens, vocab, dim, piece, int(weight_aligned), C.byref(f), C.byref(b)))
+    return f.value, b.value
+
+
+def ddp_vocab_loss_forward(hidden, hidden_stride, weight, weight_stride, dtype, ntokens, vocab, dim, targets, id_bytes,
+                           ignore_index, loss, lse, workspace, workspace_bytes, stream=None) -> None:
+    _check(lib().ddp_vocab_loss_forward(_ptr(hidden), hidden_stride, _ptr(weight), weight_stride, dtype, ntokens,
+                                        vocab, dim, _ptr(targets), id_bytes, ignore_index, _ptr(loss), _ptr(lse),
+                                        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ddp_vocab_loss_backward(hidden, hidden_stride, weight, weight_stride, dtype, ntokens, vocab, dim, targets,
+                            id_bytes, ignore_index, lse, grad_loss, grad_loss_stride, grad_hidden, gh_stride,
+                            grad_weight, gw_stride, gw_dtype, accumulate, piece, workspace, workspace_bytes,
+                            stream=None) -> None:
+    _check(lib().ddp_vocab_loss_backward(_ptr(hidden), hidden_stride, _ptr(weight), weight_stride, dtype, ntokens,
+                                         vocab, dim, _ptr(targets), id_bytes, ignore_index, _ptr(lse),
+                                         _ptr(grad_loss), grad_loss_stride, _ptr(grad_hidden), gh_stride,
+                                         _ptr(grad_weight), gw_stride, gw_dtype, int(accumulate), piece,
+                                         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ddp_lm_status(stream=None, reset=False) -> int:
+    v = C.c_int32(0)
+    _check(lib().ddp_lm_status(_stream(stream), C.byref(v), int(bool(reset))))
+    return v.value
 
 
 def ddp_set_kernel_variant(variant: int) -> None:

@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUTDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUTDIR, "libddpbucket.so")
 SOURCES = ["kernels.cu", "stream_ring.cu", "stream_fused.cu", "stream_fused_wire.cu", "stream_pack.cu", "bitmap.cu",
-           "powersgd.cu", "reducer.cpp", "assign.cpp", "plan.cpp", "timeline.cpp", "status.cpp"]
+           "powersgd.cu", "clip.cu", "embedding.cu", "vocab_loss.cu", "reducer.cpp", "assign.cpp", "plan.cpp", "timeline.cpp", "status.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,6 +34,7 @@ def _inputs() -> list[str]:
     files = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, "common.h"),
                                                         os.path.join(CSRC, "device_common.cuh"),
                                                         os.path.join(CSRC, "stream_impl.cuh"),
+                                                        os.path.join(CSRC, "lm_common.cuh"),
                                                         os.path.join(INCLUDE, "ddp_bucket.h")]
     return files
 

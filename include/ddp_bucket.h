@@ -25,9 +25,9 @@
  *     why, naming the parameter or bucket involved.  Arguments are validated on
  *     the host before anything is launched; a failed call launches nothing.
  *   - Memory: the caller owns all host and device memory.  The library
- *     allocates no device memory; its own device data are three small static
- *     arrays of the module (the status word of ddp_device_status, the
- *     streaming kernels' pool counters, and the scratch of
+ *     allocates no device memory; its own device data are four small static
+ *     arrays of the module (the status words of ddp_device_status and
+ *     ddp_lm_status, the streaming kernels' pool counters, and the scratch of
  *     ddp_powersgd_reduce_static).  A reducer owns host bookkeeping and the
  *     CUDA events it creates, released by ddp_reducer_destroy; a host front end
  *     owns two copy streams, one gate stream and its events, released by
@@ -861,6 +861,173 @@ ddp_status ddp_reducer_create_from_plan(const ddp_plan* plan, const ddp_bucket_d
                                         void* side_stream, ddp_reducer** out);
 
 void ddp_plan_destroy(ddp_plan* plan);
+
+/* ------------------------------------------------------------------------ */
+/* Language-model ends: clipping, token embedding, vocabulary loss           */
+/* ------------------------------------------------------------------------ */
+/*
+ * What a language model's step does next to the bucket reduction: the largest
+ * segments of its buckets are the embedding table's gradient and the output
+ * projection's, which the two operators below produce, and between the
+ * reduction and the optimizer the reduced gradients are clipped by their global
+ * norm.  None of the pages' arithmetic is involved.
+ *
+ * Common to these calls: matrices are row-major with a row stride in elements
+ * (>= the row length); token ids and targets are DEVICE int32 (id_bytes = 4) or
+ * int64 (id_bytes = 8); sums, norms and softmax statistics are fp32 or wider and
+ * every result is rounded once to its type; every sum is taken in an order that
+ * depends on the sizes alone, so equal calls give equal bits.  An id outside
+ * [0, vocab) cannot be refused on the host: the kernels read and write nothing
+ * through it, treat its token as described at each call, and set bit 1 of the
+ * word that ddp_lm_status reads.  `workspace` is DEVICE scratch of at least
+ * the size that the operator's size function gives, 256-byte aligned; nothing in
+ * it outlives the call's work on `stream`, and calls that may run at the same
+ * time need one each.
+ */
+enum { DDP_NORM_L2 = 0, DDP_NORM_INF = 1 };
+
+/* Bytes of workspace that ddp_grad_norm and ddp_clip_grads need. */
+enum { DDP_CLIP_WORKSPACE_BYTES = 65536 };
+
+/*
+ * ddp_grad_norm -- the global norm over many gradient tensors.
+ *
+ * DDP_NORM_L2: sqrt of the sum of squares of every element of every tensor;
+ * DDP_NORM_INF: the largest magnitude.  Squares are summed so that the result is
+ * right wherever it is a finite fp32 number, also where a square leaves fp32's
+ * range.  An infinity gives infinity, a NaN gives NaN.  No elements: 0.
+ *
+ *   grads      DEVICE table of ntensors device pointers; NULL: the tensor has no
+ *              gradient and counts as zeros.
+ *   offset     DEVICE int64[ntensors + 1], ascending, offset[0] = 0, offset[
+ *              ntensors] = total: tensor k has offset[k+1] - offset[k] contiguous
+ *              elements (lengths only: the tensors lie anywhere).
+ *   dtypes     DEVICE int32[ntensors], DDP_F32 / DDP_BF16 / DDP_F16 each.
+ *   norm       DEVICE float[1].
+ *   workspace  DEVICE, DDP_CLIP_WORKSPACE_BYTES.
+ * Errors: DDP_E_INVAL (negative sizes, NULL tables with total > 0, NULL norm or
+ * workspace, unknown norm_type, workspace_bytes too small); DDP_E_CUDA.
+ */
+ddp_status ddp_grad_norm(const void* const* grads, const int64_t* offset, const int32_t* dtypes, int32_t ntensors,
+                         int64_t total, int32_t norm_type, float* norm, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/*
+ * ddp_clip_grads -- ddp_grad_norm, then every element times
+ * min(1, max_norm / (norm + 1e-6)), rounded to the tensor's type.
+ *
+ *   out   DEVICE table of ntensors device pointers, types as grads' (NULL entry:
+ *         that tensor is not written); out == NULL: in place.  An output is its
+ *         own input or does not overlap any input.  In place, nothing is
+ *         written when the factor is 1.  A norm of infinity gives the factor 0
+ *         (infinite elements become NaN), a NaN norm makes every element NaN.
+ *   norm  DEVICE float[1]: the norm before clipping.
+ * Errors: as ddp_grad_norm; DDP_E_INVAL for a max_norm that is negative or NaN.
+ */
+ddp_status ddp_clip_grads(const void* const* grads, void* const* out, const int64_t* offset, const int32_t* dtypes,
+                          int32_t ntensors, int64_t total, int32_t norm_type, float max_norm, float* norm,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * ddp_embedding_forward -- out[t] = scale * weight[ids[t]] for ntokens tokens.
+ * A token whose id is outside [0, vocab) gets a row of zeros (and bit 1 of
+ * ddp_lm_status).  weight and out are `dtype`.
+ * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, a stride below dim, an
+ * unknown dtype or id_bytes, a NULL pointer with ntokens > 0); DDP_E_CUDA.
+ */
+ddp_status ddp_embedding_forward(const void* weight, int64_t weight_stride, int32_t dtype, int64_t vocab, int64_t dim,
+                                 const void* ids, int32_t id_bytes, int64_t ntokens, float scale, void* out,
+                                 int64_t out_stride, void* stream);
+
+/* Workspace of ddp_embedding_backward in bytes. */
+ddp_status ddp_embedding_workspace(int64_t ntokens, int64_t vocab, int64_t dim, int64_t* bytes);
+
+/*
+ * ddp_embedding_backward -- the table's gradient:
+ *   grad_weight[v] (= | +=) scale * sum of grad_out[t] over the tokens t with
+ *   ids[t] == v and v != padding_idx,
+ * summed in fp32 over the tokens sorted by id (equal ids keep their order).
+ * accumulate == 0: rows of ids that do not occur become 0; otherwise they are
+ * not touched.  padding_idx < 0: no padding.  Tokens with ids outside
+ * [0, vocab) add nothing (and set bit 1 of ddp_lm_status).
+ *   grad_out     DEVICE dtype [ntokens x dim], rows grad_stride apart.
+ *   grad_weight  DEVICE gw_dtype [vocab x dim], rows gw_stride apart; gw_dtype is
+ *                dtype or DDP_F32 (a main_grad segment).
+ * ntokens < 2^31.
+ * Errors: as ddp_embedding_forward; DDP_E_INVAL for another gw_dtype or too
+ * small a workspace.
+ */
+ddp_status ddp_embedding_backward(const void* grad_out, int64_t grad_stride, int32_t dtype, const void* ids,
+                                  int32_t id_bytes, int64_t ntokens, float scale, int64_t padding_idx, int64_t vocab,
+                                  int64_t dim, void* grad_weight, int64_t gw_stride, int32_t gw_dtype,
+                                  int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Workspace of the vocabulary loss in bytes.  piece: vocabulary words whose
+ * softmax gradient is held at a time by the backward pass (rounded up to a
+ * multiple of 256); 0: the library's choice.  weight_aligned: nonzero if the
+ * weight starts on a 16-byte boundary and its row stride is a multiple of 8
+ * elements; otherwise the calls work on an aligned copy in the workspace.
+ * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, NULL outputs).
+ */
+ddp_status ddp_vocab_loss_workspace(int64_t ntokens, int64_t vocab, int64_t dim, int64_t piece, int32_t weight_aligned,
+                                    int64_t* forward_bytes, int64_t* backward_bytes);
+
+/*
+ * ddp_vocab_loss_forward -- softmax cross entropy of z = hidden x weight^T
+ * without storing z:
+ *   lse[t] = log sum_v exp(z[t][v]),  loss[t] = lse[t] - z[t][targets[t]].
+ * A token with targets[t] == ignore_index has no part in anything: its loss and
+ * lse are 0 and its hidden state may hold anything.  A target outside
+ * [0, vocab) is treated the same way (and sets bit 1 of ddp_lm_status).
+ *   hidden   DEVICE dtype [ntokens x dim], rows hidden_stride apart.
+ *   weight   DEVICE dtype [vocab x dim], rows weight_stride apart.
+ *   loss, lse  DEVICE float[ntokens].
+ * dtype is DDP_BF16 or DDP_F16; products are exact and summed in fp32.
+ * ntokens and vocab < 2^31 - 512, dim < 2^24.
+ * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, a stride below dim,
+ * another dtype, id_bytes, a NULL pointer with ntokens > 0, too small a
+ * workspace); DDP_E_CUDA.
+ */
+ddp_status ddp_vocab_loss_forward(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
+                                  int32_t dtype, int64_t ntokens, int64_t vocab, int64_t dim, const void* targets,
+                                  int32_t id_bytes, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/*
+ * ddp_vocab_loss_backward -- gradients of sum_t grad_loss[t] * loss[t]:
+ *   G[t][v] = grad_loss[t] * (exp(z[t][v] - lse[t]) - [v == targets[t]])
+ *   grad_hidden = G x weight,   grad_weight (= | +=) G^T x hidden
+ * with z computed again and G held for one piece of the vocabulary at a time, in
+ * `dtype` after division by the largest |grad_loss| (exactly that factor is
+ * put back in fp32).  Ignored tokens get rows of zeros in grad_hidden.
+ *   lse          what ddp_vocab_loss_forward wrote.
+ *   grad_loss    DEVICE float, element t at grad_loss[t * grad_loss_stride];
+ *                grad_loss_stride is 1, or 0 for one value for every token.
+ *   grad_hidden  DEVICE dtype [ntokens x dim], rows gh_stride apart; NULL: not
+ *                wanted.
+ *   grad_weight  DEVICE gw_dtype [vocab x dim], rows gw_stride apart; gw_dtype is
+ *                dtype or DDP_F32; NULL: not wanted.
+ * Errors: as the forward; DDP_E_INVAL for another gw_dtype, grad_loss_stride, or
+ * both outputs NULL.
+ */
+ddp_status ddp_vocab_loss_backward(const void* hidden, int64_t hidden_stride, const void* weight,
+                                   int64_t weight_stride, int32_t dtype, int64_t ntokens, int64_t vocab, int64_t dim,
+                                   const void* targets, int32_t id_bytes, int64_t ignore_index, const float* lse,
+                                   const float* grad_loss, int32_t grad_loss_stride, void* grad_hidden,
+                                   int64_t gh_stride, void* grad_weight, int64_t gw_stride, int32_t gw_dtype,
+                                   int32_t accumulate, int64_t piece, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * ddp_lm_status -- the status word of the embedding and vocabulary-loss calls:
+ * 0 normally; bit 0 set if a kernel gave up on an mbarrier wait (about 2 s) and
+ * returned with its outputs incomplete; bit 1 set if a token id or target lay
+ * outside [0, vocab) (other than ignore_index).  Reads the word on `stream`
+ * (synchronising that stream); reset != 0 clears it.
+ * HOST out: *status.  Errors: DDP_E_INVAL (NULL status); DDP_E_CUDA.
+ */
+ddp_status ddp_lm_status(void* stream, int32_t* status, int32_t reset);
 
 /* ------------------------------------------------------------------------ */
 /* Kernel variants and device status                                         */
