@@ -35,6 +35,7 @@ def _inputs() -> list[str]:
                                                         os.path.join(CSRC, "device_common.cuh"),
                                                         os.path.join(CSRC, "stream_impl.cuh"),
                                                         os.path.join(CSRC, "lm_common.cuh"),
+                                                        os.path.join(CSRC, "umma.cuh"),
                                                         os.path.join(INCLUDE, "ddp_bucket.h")]
     return files
 

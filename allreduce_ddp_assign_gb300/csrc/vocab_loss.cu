@@ -13,15 +13,16 @@
 // gathered into consecutive rows, so masked-word training pays for the masked
 // words only and nothing an ignored row holds can reach a result.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "lm_common.cuh"
+#include "umma.cuh"
 
 namespace ddplm {
 namespace {
 
 constexpr int kRowTile = 256;   // rows of the gathered arrays are padded to this
-constexpr int kTileM = 64, kTileN = 64, kTileK = 16;
 constexpr int kPrepThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -42,7 +43,7 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     Space s{};
     s.tpad = round_up(std::max<int64_t>(T, 1), kRowTile);
     s.dpad = round_up(D, 8);
-    s.ntiles = (V + kTileN - 1) / kTileN;
+    s.ntiles = (V + 127) / 128;  // one pair of statistics a row for each 128 words
     const int64_t vpad = round_up(V, 256);
     if (piece <= 0) piece = std::max<int64_t>(1024, (int64_t{1} << 27) / s.tpad);
     s.piece = std::min(vpad, round_up(piece, 256));
@@ -61,7 +62,7 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
         s.ratio = take(4 * s.tpad);
         s.lse = take(4 * s.tpad);
         s.grad = take(2 * s.tpad * s.piece);
-        s.acc = take(s.piece < vpad ? 4 * s.tpad * D : 0);
+        s.acc = take(s.piece < vpad ? 4 * s.tpad * s.dpad : 0);
     } else {
         s.part = take(8 * s.tpad * s.ntiles);
         s.ztarget = take(4 * s.tpad);
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
             for (int64_t c = lane; c < a.dim; c += 32) dst[c] = 0;
         }
     }
-    // rows up to the tile's end are zeros: they are terms of dW's sums
-    const int end = (all + kRowTile - 1) / kRowTile * kRowTile;
+    // rows up to the tile's end are zeros (past the T-th the copies supply them): they are terms of dW's sums
+    const int end = min(a.T, (all + kRowTile - 1) / kRowTile * kRowTile);
     for (int r = all + blockIdx.x; r < end; r += gridDim.x)
         for (int64_t c = tid; c < a.dpad; c += kPrepThreads) a.out[static_cast<int64_t>(r) * a.dpad + c] = 0;
 }
@@ -207,18 +208,35 @@ copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, ui
 // ---------------------------------------------------------------------------
 // products: C[m][n] = sum_k A[m][k] B[n][k], and what is done with C
 // ---------------------------------------------------------------------------
+// Two CTAs on a pair of SMs share one 256 x 256 tile of C: each holds 128 rows of
+// A and 128 of B in shared memory and 128 rows of C in tensor memory, and one
+// thread of the first CTA issues the products of both.  Per CTA:
+//   warp 8     copies 128 x 64 boxes of A and B into a ring of stages;
+//   warp 9     (first CTA) issues four k = 16 products a stage;
+//   warps 0-7  take finished tiles out of tensor memory, which holds two, so that
+//              a tile's epilogue runs under the next tile's products.
+// The grid is one pair of CTAs for each pair of SMs; a pair takes every npairs-th tile.
 enum Use { USE_STATS, USE_GRAD, USE_DH, USE_DW };
 
+constexpr int kTile = 256;               // rows and columns of a pair's tile
+constexpr int kHalf = 128;               // rows of A, of B and of C that one CTA holds
+constexpr int kBlockK = 64;              // one 128-byte row of 16-bit values
+constexpr int kStages = 6;
+constexpr int kOperandBytes = kHalf * kBlockK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8;
+constexpr int kStagingBytes = 4096;      // per epilogue warp: 32 rows of 128 bytes
+constexpr int kProductThreads = 32 * (kEpiWarps + 2);
+constexpr int kProductSmem = kStages * kStageBytes + kEpiWarps * kStagingBytes + 1024;
+
 struct Product {
-    const void* a;
-    int64_t am, ak;       // strides of A in elements
-    const void* b;
-    int64_t bn, bk;
+    CUtensorMap ta, tb;
     int64_t M, N, K;
     const int32_t* count; // gathered rows: bounds M (STATS, GRAD, DH) or K (DW)
+    int64_t rows_cap;     // rows of the gathered arrays that exist
     int64_t v0;           // first word of the piece
-    int64_t vocab;
     const int32_t* target;
+    int* status;
     // STATS
     float2* part;
     int64_t tpad;
@@ -236,119 +254,437 @@ struct Product {
     const int32_t* rows;
     void* out;
     int64_t os;
-    int32_t out_f32, accumulate;
+    int32_t out_f32, accumulate, vec;
 };
 
-template <int DT, int USE> __global__ void __launch_bounds__(256) product_kernel(Product p)
+template <int USE> struct Majors {
+    static constexpr bool a_mn = USE == USE_DW;
+    static constexpr bool b_mn = USE == USE_DH || USE == USE_DW;
+};
+
+// one CTA's 128 rows of an operand, 64 of k: one box, or two where m (n) is contiguous
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int k, uint32_t bar)
+{
+    if (MN) {
+        tensor_load(dst, map, row, k, bar);
+        tensor_load(dst + kOperandBytes / 2, map, row + 64, k, bar);
+    } else {
+        tensor_load(dst, map, k, row, bar);
+    }
+}
+// descriptor of k = 16 values at step j of a stage
+template <bool MN> __device__ __forceinline__ uint64_t step_desc(uint32_t base, int j)
+{
+    return MN ? operand_desc(base + j * 2048, kOperandBytes / 2, 1024) : operand_desc(base + j * 32, 16, 1024);
+}
+
+__device__ __forceinline__ void tile_values(uint32_t taddr, bool empty, float (&c)[32])
+{
+    uint32_t v[32];
+    if (empty) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) c[j] = 0.f;
+        return;
+    }
+    tmem_load32(taddr, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) c[j] = __uint_as_float(v[j]);
+}
+
+// 16-byte chunk `ch` (of 8) of row r in a warp's staging area, spread over the banks
+__device__ __forceinline__ uint32_t staged(uint32_t base, int r, int ch) { return base + r * 128 + ((ch ^ (r & 7)) << 4); }
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    typename Elem<DT>::T x[2] = {Elem<DT>::from_f(a), Elem<DT>::from_f(b)};
+    return *reinterpret_cast<uint32_t*>(x);
+}
+
+template <int DT, int USE>
+__device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool empty, int64_t m0, int64_t n0, int64_t M,
+                                         uint32_t staging, int half, int lane)
 {
     using T = typename Elem<DT>::T;
-    __shared__ float sa[kTileK][kTileM + 1], sb[kTileK][kTileN + 1];
-    __shared__ float2 red[kTileM][17];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int64_t m = m0 + lane;  // this thread's row; n0: the warp's first of 128 columns
+    float c[32];
+    if (USE == USE_STATS) {
+        float mx = -INFINITY, s = 0.f;
+        const bool in = m < M;
+        const int64_t y = in ? p.target[m] : -1;
+        for (int q = 0; q < 4; ++q) {
+            tile_values(taddr + q * 32, empty, c);
+            const int64_t n = n0 + q * 32;
+            if (n >= p.N) break;
+            if (n + 32 > p.N) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) c[j] = n + j < p.N ? c[j] : -INFINITY;
+            }
+            if (y >= n && y < n + 32) {
+                float z = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z = y - n == j ? c[j] : z;
+                p.ztarget[m] = z;
+            }
+            float cm = c[0];
+#pragma unroll
+            for (int j = 1; j < 32; ++j) cm = fmaxf(cm, c[j]);
+            const float top = fmaxf(mx, cm);
+            if (top != -INFINITY) {  // all of them minus infinity: they add nothing
+                const float shift = top * kLog2e;
+                s *= mx == -INFINITY ? 0.f : exp2f(mx * kLog2e - shift);
+                float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    a0 += exp2f(fmaf(c[j], kLog2e, -shift));
+                    a1 += exp2f(fmaf(c[j + 1], kLog2e, -shift));
+                }
+                s += a0 + a1;
+                mx = top;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s += c[j] != c[j] ? c[j] : 0.f;  // a NaN among them stays
+            }
+        }
+        if (in && n0 < p.N) p.part[(n0 >> 7) * p.tpad + m] = make_float2(mx, s);
+    } else if (USE == USE_GRAD) {
+        const bool in = m < M;
+        const float shift = in ? p.lse[m] * kLog2e : 0.f;
+        const float ratio = in ? p.ratio[m] : 0.f;
+        const int64_t y = in ? p.target[m] - p.v0 : -1;
+        for (int q = 0; q < 2; ++q) {
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = n0 + q * 64 + h * 32;
+                tile_values(taddr + q * 64 + h * 32, empty, c);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) c[j] = exp2f(fmaf(c[j], kLog2e, -shift));
+                if (y >= n && y < n + 32) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) c[j] -= y - n == j ? 1.f : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) c[j] = ratio == 0.f ? 0.f : c[j] * ratio;
+                if (n + 32 > p.N) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) c[j] = n + j < p.N ? c[j] : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sts16(staged(staging, lane, h * 4 + k),
+                          make_uint4(pack2<DT>(c[8 * k], c[8 * k + 1]), pack2<DT>(c[8 * k + 2], c[8 * k + 3]),
+                                     pack2<DT>(c[8 * k + 4], c[8 * k + 5]), pack2<DT>(c[8 * k + 6], c[8 * k + 7])));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3), ch = lane & 7;
+                if (m0 + r < p.rows_cap)
+                    *reinterpret_cast<uint4*>(static_cast<T*>(p.g) + (m0 + r) * p.gld + n0 + q * 64 + ch * 8) =
+                        lds16(staged(staging, r, ch));
+            }
+            __syncwarp();
+        }
+    } else {
+        const float alpha = *p.gmax * p.inv_scale;
+        for (int q = 0; q < 4; ++q) {
+            tile_values(taddr + q * 32, empty, c);
+            if (n0 + q * 32 >= p.N) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sts16(staged(staging, lane, k), make_uint4(__float_as_uint(c[4 * k]), __float_as_uint(c[4 * k + 1]),
+                                                           __float_as_uint(c[4 * k + 2]), __float_as_uint(c[4 * k + 3])));
+            __syncwarp();
+            const int64_t n = n0 + q * 32 + (lane & 7) * 4;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3);
+                const uint4 raw = lds16(staged(staging, r, lane & 7));
+                float x[4] = {__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w)};
+                const int64_t row = m0 + r;
+                if (row >= M || n >= p.N) continue;
+                const int width = static_cast<int>(min(static_cast<int64_t>(4), p.N - n));
+                if (USE == USE_DH && p.acc) {
+                    float* a = p.acc + row * p.tpad + n;  // tpad: the sums' row stride, a multiple of 4
+                    if (!p.first) {
+                        const float4 o = *reinterpret_cast<const float4*>(a);
+                        x[0] += o.x; x[1] += o.y; x[2] += o.z; x[3] += o.w;
+                    }
+                    if (!p.last) {
+                        *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]);
+                        continue;
+                    }
+                }
+                const int64_t at = (USE == USE_DH ? p.rows[row] : p.v0 + row) * p.os + n;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] *= alpha;
+                if (USE == USE_DW && p.out_f32) {
+                    float* o = static_cast<float*>(p.out) + at;
+                    if (p.vec && width == 4) {
+                        if (p.accumulate) {
+                            const float4 v = *reinterpret_cast<const float4*>(o);
+                            x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
+                        }
+                        *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+                    } else {
+                        for (int j = 0; j < width; ++j) o[j] = x[j] + (p.accumulate ? o[j] : 0.f);
+                    }
+                } else {
+                    T* o = static_cast<T*>(p.out) + at;
+                    if (p.vec && width == 4) {
+                        if (USE == USE_DW && p.accumulate) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(o);
+                            const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[j] += Elem<DT>::to_f(t[j]);
+                        }
+                        *reinterpret_cast<uint2*>(o) = make_uint2(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]));
+                    } else {
+                        for (int j = 0; j < width; ++j)
+                            o[j] = Elem<DT>::from_f(x[j] + (USE == USE_DW && p.accumulate ? Elem<DT>::to_f(o[j]) : 0.f));
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+template <int DT, int USE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product p)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int dead;
+    const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_addr(bars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto tfull = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+    auto tempty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+
+    if (threadIdx.x == 0) {
+        dead = 0;
+        for (int s = 0; s < kStages; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(tfull(b), 1);
+            bar_init(tempty(b), 2 * kEpiWarps);
+        }
+        bar_init_fence();
+        tensor_map_prefetch(&p.ta);
+        tensor_map_prefetch(&p.tb);
+    }
+    if (warp == 9) tmem_alloc(smem_addr(&tmem_base), 512);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base;
+
     const int64_t count = *p.count;
     const int64_t M = USE == USE_DW ? p.M : min(p.M, count);
     const int64_t K = USE == USE_DW ? min(p.K, count) : p.K;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTileM, n0 = static_cast<int64_t>(blockIdx.x) * kTileN;
-    const int64_t mend = USE == USE_GRAD ? (count + kRowTile - 1) / kRowTile * kRowTile : M;
-    if (m0 >= mend) return;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kTileK) {
-        for (int i = tid; i < kTileM * kTileK; i += 256) {
-            const int m = p.ak == 1 ? i / kTileK : i % kTileM, k = p.ak == 1 ? i % kTileK : i / kTileM;
-            sa[k][m] = (m0 + m < M && k0 + k < K) ? Elem<DT>::to_f(static_cast<const T*>(p.a)[(m0 + m) * p.am + (k0 + k) * p.ak]) : 0.f;
-        }
-        for (int i = tid; i < kTileN * kTileK; i += 256) {
-            const int n = p.bk == 1 ? i / kTileK : i % kTileN, k = p.bk == 1 ? i % kTileK : i / kTileN;
-            sb[k][n] = (n0 + n < p.N && k0 + k < K) ? Elem<DT>::to_f(static_cast<const T*>(p.b)[(n0 + n) * p.bn + (k0 + k) * p.bk]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kTileK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-    if (USE == USE_STATS) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + ty * 4 + i;
-            float mx = -INFINITY, s = 0.f;
-            for (int j = 0; j < 4; ++j)
-                if (n0 + tx * 4 + j < p.N) mx = fmaxf(mx, acc[i][j]);
-            for (int j = 0; j < 4; ++j)
-                if (n0 + tx * 4 + j < p.N) {
-                    s += mx == -INFINITY ? 0.f : exp2f((acc[i][j] - mx) * kLog2e);
-                    if (m < M && p.target[m] == n0 + tx * 4 + j) p.ztarget[m] = acc[i][j];
-                }
-            red[ty * 4 + i][tx] = make_float2(mx, s);
-        }
-        __syncthreads();
-        if (tid < kTileM && m0 + tid < M) {
-            float mx = -INFINITY, s = 0.f;
-            for (int j = 0; j < 16; ++j) mx = fmaxf(mx, red[tid][j].x);
-            for (int j = 0; j < 16; ++j)
-                if (red[tid][j].x != -INFINITY) s += red[tid][j].y * exp2f((red[tid][j].x - mx) * kLog2e);
-            p.part[blockIdx.x * p.tpad + m0 + tid] = make_float2(mx, s);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            const float c = acc[i][j];
-            if (USE == USE_GRAD) {
-                float g = 0.f;  // rows and words beyond the end are zeros
-                if (m < M && n < p.N) {
-                    g = exp2f((c - p.lse[m]) * kLog2e) - (p.target[m] == p.v0 + n ? 1.f : 0.f);
-                    g = p.ratio[m] == 0.f ? 0.f : g * p.ratio[m];
-                }
-                if (n < p.gld) static_cast<T*>(p.g)[m * p.gld + n] = Elem<DT>::from_f(g);
-            } else if (m < M && n < p.N) {
-                const float alpha = *p.gmax * p.inv_scale;
-                if (USE == USE_DH) {
-                    float s = c;
-                    if (p.acc) {
-                        if (!p.first) s += p.acc[m * p.N + n];
-                        if (!p.last) p.acc[m * p.N + n] = s;
-                    }
-                    if (p.last) static_cast<T*>(p.out)[p.rows[m] * p.os + n] = Elem<DT>::from_f(s * alpha);
-                } else if (p.out_f32) {
-                    float* o = static_cast<float*>(p.out) + (p.v0 + m) * p.os + n;
-                    *o = c * alpha + (p.accumulate ? *o : 0.f);
-                } else {
-                    T* o = static_cast<T*>(p.out) + (p.v0 + m) * p.os + n;
-                    *o = Elem<DT>::from_f(c * alpha + (p.accumulate ? Elem<DT>::to_f(*o) : 0.f));
+    const int mt = static_cast<int>((M + kTile - 1) / kTile), nt = static_cast<int>((p.N + kTile - 1) / kTile);
+    const int nkb = static_cast<int>((K + kBlockK - 1) / kBlockK);
+    const int64_t tiles = static_cast<int64_t>(mt) * nt;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (warp == 8) {
+        if (lane == 0 && nkb > 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = pair; ok && t < tiles; t += npairs) {
+                const int m = static_cast<int>(t % mt) * kTile + static_cast<int>(rank) * kHalf;
+                const int n = static_cast<int>(t / mt) * kTile + static_cast<int>(rank) * kHalf;
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!(ok = bar_wait(empty(s), ((it / kStages) & 1) ^ 1, &dead))) break;
+                    // both CTAs' bytes are counted on the first CTA's barrier
+                    if (rank == 0) bar_expect(full(s), 2 * kStageBytes);
+                    const uint32_t bar = cluster_addr(full(s), 0);
+                    const uint32_t a = base + s * kStageBytes;
+                    load_operand<Majors<USE>::a_mn>(a, &p.ta, m, kb * kBlockK, bar);
+                    load_operand<Majors<USE>::b_mn>(a + kOperandBytes, &p.tb, n, kb * kBlockK, bar);
                 }
             }
+            // the last arrivals on this CTA's barriers come before it may leave
+            for (int i = 0; ok && i < kStages; ++i, ++it) ok = bar_wait(empty(it % kStages), ((it / kStages) & 1) ^ 1, &dead);
         }
+    } else if (warp == 9) {
+        if (rank == 0 && lane == 0 && nkb > 0) {
+            constexpr uint32_t desc = product_desc(DT == DDP_BF16, Majors<USE>::a_mn, Majors<USE>::b_mn, kTile, kTile);
+            uint32_t it = 0, j = 0;
+            bool ok = true;
+            for (int64_t t = pair; ok && t < tiles; t += npairs, ++j) {
+                const int b = j & 1;
+                if (!(ok = bar_wait(tempty(b), ((j >> 1) & 1) ^ 1, &dead))) break;
+                tmem_fence_after();
+                const uint32_t d = tmem + b * kTile;
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!(ok = bar_wait(full(s), (it / kStages) & 1, &dead))) break;
+                    tmem_fence_after();
+                    const uint32_t a = base + s * kStageBytes;
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 16; ++k)
+                        product_pair(d, step_desc<Majors<USE>::a_mn>(a, k), step_desc<Majors<USE>::b_mn>(a + kOperandBytes, k),
+                                     desc, kb > 0 || k > 0);
+                    product_commit(empty(s));
+                }
+                if (ok) product_commit(tfull(b));
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t staging = base + kStages * kStageBytes + warp * kStagingBytes;
+        uint32_t j = 0;
+        for (int64_t t = pair; t < tiles; t += npairs, ++j) {
+            const int b = j & 1;
+            if (nkb > 0) {
+                if (!__all_sync(0xffffffffu, bar_wait(tfull(b), (j >> 1) & 1, &dead))) break;
+                tmem_fence_after();
+            }
+            const int64_t m0 = (t % mt) * kTile + rank * kHalf + quarter * 32;
+            const int64_t n0 = (t / mt) * kTile + half * kHalf;
+            __syncwarp();
+            epilogue<DT, USE>(p, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * kTile + half * kHalf, nkb == 0, m0,
+                              n0, M, staging, half, lane);
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0 && nkb > 0) bar_arrive_cluster(cluster_addr(tempty(b), 0));
+        }
+    }
+    __syncthreads();
+    if (dead) {
+        // a wait gave up: report it, and let copies and products in flight end before the memory is given back
+        if (threadIdx.x == 0) {
+            atomicOr(p.status, kErrWait);
+            const uint64_t t0 = clock_ns();
+            for (uint32_t i = 0; i < (1u << 24) && clock_ns() - t0 < 20000000ull; ++i) {}
+        }
+        __syncthreads();
+    }
+    tmem_fence_before();
+    cluster_sync();
+    tmem_fence_after();
+    if (warp == 9) tmem_free(tmem, 512);
 }
 
-template <int DT, int USE> void launch_product(const Product& p, cudaStream_t s)
+// A matrix of 16-bit values, `inner` contiguous values a row, cut in boxes of 64 values by `box_rows` rows.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
 {
-    const dim3 grid(static_cast<unsigned>((p.N + kTileN - 1) / kTileN), static_cast<unsigned>((p.M + kTileM - 1) / kTileM));
-    product_kernel<DT, USE><<<grid, 256, 0, s>>>(p);
+    static std::atomic<void*> cached{nullptr};
+    void* f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        cached.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeFn>(f);
 }
 
-// join the tiles' (maximum, sum) pairs of each gathered row
-__global__ void __launch_bounds__(256)
-combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, int64_t tpad, int64_t ntiles,
+bool make_map(CUtensorMap* map, int dtype, const void* ptr, int64_t inner, int64_t rows, int64_t stride, int box_rows)
+{
+    const EncodeFn f = encode_fn();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {kBlockK, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t unit[2] = {1, 1};
+    return f(map, dtype == DDP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+             const_cast<void*>(ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// the operands' maps: A is [M x K] and B [N x K] seen as stored, `*_stride` between stored rows
+template <int DT, int USE>
+cudaError_t launch_product(Product& p, const void* a, int64_t a_stride, const void* b, int64_t b_stride, cudaStream_t s)
+{
+    static std::atomic<int> cached[ddp::kMaxDevices] = {};
+    if (Majors<USE>::a_mn ? !make_map(&p.ta, DT, a, p.M, p.K, a_stride, kBlockK) : !make_map(&p.ta, DT, a, p.K, p.M, a_stride, kHalf))
+        return cudaErrorInvalidValue;
+    if (Majors<USE>::b_mn ? !make_map(&p.tb, DT, b, p.N, p.K, b_stride, kBlockK) : !make_map(&p.tb, DT, b, p.K, p.N, b_stride, kHalf))
+        return cudaErrorInvalidValue;
+    const int dev = ddp::current_device();
+    int pairs = dev >= 0 ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (!pairs) {
+        cudaError_t e = cudaFuncSetAttribute(product_kernel<DT, USE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kProductThreads);
+        cfg.dynamicSmemBytes = kProductSmem;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 2;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&pairs, product_kernel<DT, USE>, &cfg);
+        if (e != cudaSuccess) return e;
+        pairs = std::max(1, std::min(pairs, ddp::device_sm_count() / 2));
+        if (dev >= 0) cached[dev].store(pairs, std::memory_order_relaxed);
+    }
+    const int64_t tiles = ((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
+    const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, pairs));
+    product_kernel<DT, USE><<<grid, kProductThreads, kProductSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+// joins the (maximum, sum) pairs of each gathered row: 32 threads a row, in a fixed order
+constexpr int kJoinRows = 8;
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    // a side whose words are all minus infinity brings 0 (or a NaN, which stays)
+    const float sa = a.x == -INFINITY ? a.y : a.y * exp2f((a.x - m) * kLog2e);
+    const float sb = b.x == -INFINITY ? b.y : b.y * exp2f((b.x - m) * kLog2e);
+    return make_float2(m, sa + sb);
+}
+__global__ void __launch_bounds__(32 * kJoinRows)
+combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, int64_t tpad, int ntiles,
                const float* ztarget, float* loss, float* lse)
 {
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (m >= *count) return;
-    float mx = -INFINITY, s = 0.f;
-    for (int64_t j = 0; j < ntiles; ++j) mx = fmaxf(mx, part[j * tpad + m].x);
-    for (int64_t j = 0; j < ntiles; ++j) {
-        const float2 q = part[j * tpad + m];
-        if (q.x != -INFINITY) s += q.y * exp2f((q.x - mx) * kLog2e);
+    __shared__ float2 sh[32][kJoinRows];
+    const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
+    const bool in = m < *count;
+    float2 q = make_float2(-INFINITY, 0.f);
+    if (in) {
+#pragma unroll 4
+        for (int j = g; j < ntiles; j += 32) q = join_pairs(q, part[j * tpad + m]);
     }
-    const float l = mx + logf(s);
-    lse[rows[m]] = l;
-    loss[rows[m]] = l - ztarget[m];
+    sh[g][r] = q;
+    for (int o = 16; o; o >>= 1) {
+        __syncthreads();
+        if (g < o) sh[g][r] = join_pairs(sh[g][r], sh[g + o][r]);
+    }
+    if (g == 0 && in) {
+        const float l = sh[0][r].x + logf(sh[0][r].y);
+        lse[rows[m]] = l;
+        loss[rows[m]] = l - ztarget[m];
+    }
 }
 
 struct Call {
@@ -414,7 +750,7 @@ void launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, int* stat
     }
 }
 
-template <int DT> void run_forward(const Call& c, const Space& sp, char* w, int* status, float* loss, float* lse, cudaStream_t s)
+template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* w, int* status, float* loss, float* lse, cudaStream_t s)
 {
     PrepArgs a{};
     a.loss = loss;
@@ -423,21 +759,22 @@ template <int DT> void run_forward(const Call& c, const Space& sp, char* w, int*
     int64_t ws;
     launch_prep(a, c, sp, w, status, s, &weight, &ws);
     Product p{};
-    p.a = a.out; p.am = sp.dpad; p.ak = 1;
-    p.b = weight; p.bn = ws; p.bk = 1;
     p.M = c.T; p.N = c.V; p.K = c.D;
     p.count = a.count;
-    p.vocab = c.V;
     p.target = a.target;
+    p.status = status;
     p.part = reinterpret_cast<float2*>(w + sp.part);
     p.tpad = sp.tpad;
     p.ztarget = reinterpret_cast<float*>(w + sp.ztarget);
-    launch_product<DT, USE_STATS>(p, s);
-    combine_kernel<<<static_cast<unsigned>((c.T + 255) / 256), 256, 0, s>>>(a.count, a.rows, p.part, sp.tpad, sp.ntiles, p.ztarget, loss, lse);
+    const cudaError_t e = launch_product<DT, USE_STATS>(p, a.out, sp.dpad, weight, ws, s);
+    if (e != cudaSuccess) return e;
+    combine_kernel<<<static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows), 32 * kJoinRows, 0, s>>>(
+        a.count, a.rows, p.part, sp.tpad, static_cast<int>(sp.ntiles), p.ztarget, loss, lse);
+    return cudaGetLastError();
 }
 
 template <int DT>
-void run_backward(const Call& c, const Space& sp, char* w, int* status, const float* lse, const float* gl, int gl_stride,
+cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, const float* lse, const float* gl, int gl_stride,
                   void* gh, int64_t ghs, void* gw, int64_t gws, int gw_f32, int accumulate, cudaStream_t s)
 {
     PrepArgs a{};
@@ -458,7 +795,8 @@ void run_backward(const Call& c, const Space& sp, char* w, int* status, const fl
         const char* wp = static_cast<const char*>(weight) + 2 * v0 * ws;
         Product p{};
         p.count = a.count;
-        p.vocab = c.V;
+        p.rows_cap = c.T;
+        p.status = status;
         p.v0 = v0;
         p.target = a.target;
         p.lse = a.lse;
@@ -468,31 +806,30 @@ void run_backward(const Call& c, const Space& sp, char* w, int* status, const fl
         p.gmax = a.gmax;
         p.inv_scale = 1.f / g_scale<DT>();
         p.rows = a.rows;
+        p.tpad = sp.dpad;
         Product q = p;
-        q.a = a.out; q.am = sp.dpad; q.ak = 1;
-        q.b = wp; q.bn = ws; q.bk = 1;
-        q.M = sp.tpad; q.N = words; q.K = c.D;
-        launch_product<DT, USE_GRAD>(q, s);
-        if (gh) {
+        q.M = c.T; q.N = words; q.K = c.D;
+        cudaError_t e = launch_product<DT, USE_GRAD>(q, a.out, sp.dpad, wp, ws, s);
+        if (e == cudaSuccess && gh) {
             q = p;
-            q.a = p.g; q.am = p.gld; q.ak = 1;
-            q.b = wp; q.bn = 1; q.bk = ws;
             q.M = c.T; q.N = c.D; q.K = words;
             q.first = v0 == 0;
             q.last = v0 + words == c.V;
             q.acc = q.first && q.last ? nullptr : reinterpret_cast<float*>(w + sp.acc);
             q.out = gh; q.os = ghs;
-            launch_product<DT, USE_DH>(q, s);
+            q.vec = aligned16(gh) && ghs % 4 == 0;
+            e = launch_product<DT, USE_DH>(q, p.g, p.gld, wp, ws, s);
         }
-        if (gw) {
+        if (e == cudaSuccess && gw) {
             q = p;
-            q.a = p.g; q.am = 1; q.ak = p.gld;
-            q.b = a.out; q.bn = 1; q.bk = sp.dpad;
-            q.M = words; q.N = c.D; q.K = sp.tpad;
+            q.M = words; q.N = c.D; q.K = c.T;
             q.out = gw; q.os = gws; q.out_f32 = gw_f32; q.accumulate = accumulate;
-            launch_product<DT, USE_DW>(q, s);
+            q.vec = aligned16(gw) && gws % 4 == 0;
+            e = launch_product<DT, USE_DW>(q, p.g, p.gld, a.out, sp.dpad, s);
         }
+        if (e != cudaSuccess) return e;
     }
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -533,9 +870,8 @@ extern "C" ddp_status ddp_vocab_loss_forward(const void* hidden, int64_t hidden_
     if (!status) return ddp::fail(DDP_E_CUDA, "%s: the status word is unavailable", fn);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* w = static_cast<char*>(workspace);
-    if (dtype == DDP_BF16) run_forward<DDP_BF16>(c, sp, w, status, loss, lse, s);
-    else run_forward<DDP_F16>(c, sp, w, status, loss, lse, s);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = dtype == DDP_BF16 ? run_forward<DDP_BF16>(c, sp, w, status, loss, lse, s)
+                                              : run_forward<DDP_F16>(c, sp, w, status, loss, lse, s);
     if (err != cudaSuccess) return ddp::fail(DDP_E_CUDA, "%s: kernel launch failed: %s", fn, cudaGetErrorString(err));
     return ddp::ok();
 }
@@ -578,11 +914,11 @@ extern "C" ddp_status ddp_vocab_loss_backward(const void* hidden, int64_t hidden
     if (!status) return fail(DDP_E_CUDA, "%s: the status word is unavailable", fn);
     char* w = static_cast<char*>(workspace);
     const int f32 = gw_dtype == DDP_F32;
-    if (dtype == DDP_BF16)
-        run_backward<DDP_BF16>(c, sp, w, status, lse, grad_loss, grad_loss_stride, grad_hidden, gh_stride, grad_weight, gw_stride, f32, accumulate != 0, s);
-    else
-        run_backward<DDP_F16>(c, sp, w, status, lse, grad_loss, grad_loss_stride, grad_hidden, gh_stride, grad_weight, gw_stride, f32, accumulate != 0, s);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err =
+        dtype == DDP_BF16 ? run_backward<DDP_BF16>(c, sp, w, status, lse, grad_loss, grad_loss_stride, grad_hidden, gh_stride,
+                                                   grad_weight, gw_stride, f32, accumulate != 0, s)
+                          : run_backward<DDP_F16>(c, sp, w, status, lse, grad_loss, grad_loss_stride, grad_hidden, gh_stride,
+                                                  grad_weight, gw_stride, f32, accumulate != 0, s);
     if (err != cudaSuccess) return fail(DDP_E_CUDA, "%s: kernel launch failed: %s", fn, cudaGetErrorString(err));
     return ddp::ok();
 }
