@@ -662,28 +662,56 @@ __device__ __forceinline__ float2 join_pairs(float2 a, float2 b)
     const float sb = b.x == -INFINITY ? b.y : b.y * exp2f((b.x - m) * kLog2e);
     return make_float2(m, sa + sb);
 }
+// The target's logit is computed again with fp32 multiply-adds: the tensor cores cut
+// off low bits at each step of k, and a loss is a small difference of two logits.
+// Both places it enters by take the better value: loss = lse - z_y, and lse itself,
+// moved by p_y (z_y - what the tile had).
+template <int DT>
 __global__ void __launch_bounds__(32 * kJoinRows)
 combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, int64_t tpad, int ntiles,
-               const float* ztarget, float* loss, float* lse)
+               const float* ztarget, const void* hidden, int64_t dpad, const void* weight, int64_t ws, int64_t dim,
+               const int32_t* target, float* loss, float* lse)
 {
+    using T = typename Elem<DT>::T;
     __shared__ float2 sh[32][kJoinRows];
+    __shared__ float dot[32][kJoinRows];
     const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
     const int64_t m = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
     const bool in = m < *count;
     float2 q = make_float2(-INFINITY, 0.f);
+    float d = 0.f;
     if (in) {
+        const T* h = static_cast<const T*>(hidden) + m * dpad;
+        const T* w = static_cast<const T*>(weight) + target[m] * ws;
+        const int64_t whole = dim / 8 * 8;
+#pragma unroll 4
+        for (int64_t c = g * 8; c < whole; c += 256) {
+            const Vec<DT> x = *reinterpret_cast<const Vec<DT>*>(h + c), y = *reinterpret_cast<const Vec<DT>*>(w + c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d = fmaf(Elem<DT>::to_f(x.v[j]), Elem<DT>::to_f(y.v[j]), d);
+        }
+        if (whole + g < dim) d = fmaf(Elem<DT>::to_f(h[whole + g]), Elem<DT>::to_f(w[whole + g]), d);
 #pragma unroll 4
         for (int j = g; j < ntiles; j += 32) q = join_pairs(q, part[j * tpad + m]);
     }
     sh[g][r] = q;
+    dot[g][r] = d;
     for (int o = 16; o; o >>= 1) {
         __syncthreads();
-        if (g < o) sh[g][r] = join_pairs(sh[g][r], sh[g + o][r]);
+        if (g < o) {
+            sh[g][r] = join_pairs(sh[g][r], sh[g + o][r]);
+            dot[g][r] += dot[g + o][r];
+        }
     }
     if (g == 0 && in) {
-        const float l = sh[0][r].x + logf(sh[0][r].y);
+        float l = sh[0][r].x + logf(sh[0][r].y), z = ztarget[m];
+        const float delta = dot[0][r] - z;
+        if (fabsf(delta) < 1.f) {  // not where a logit is infinite or NaN
+            l += exp2f((z - l) * kLog2e) * delta;
+            z = dot[0][r];
+        }
         lse[rows[m]] = l;
-        loss[rows[m]] = l - ztarget[m];
+        loss[rows[m]] = l - z;
     }
 }
 
@@ -768,8 +796,9 @@ template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* 
     p.ztarget = reinterpret_cast<float*>(w + sp.ztarget);
     const cudaError_t e = launch_product<DT, USE_STATS>(p, a.out, sp.dpad, weight, ws, s);
     if (e != cudaSuccess) return e;
-    combine_kernel<<<static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows), 32 * kJoinRows, 0, s>>>(
-        a.count, a.rows, p.part, sp.tpad, static_cast<int>(sp.ntiles), p.ztarget, loss, lse);
+    combine_kernel<DT><<<static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows), 32 * kJoinRows, 0, s>>>(
+        a.count, a.rows, p.part, sp.tpad, static_cast<int>(sp.ntiles), p.ztarget, a.out, sp.dpad, weight, ws, c.D, a.target,
+        loss, lse);
     return cudaGetLastError();
 }
 
