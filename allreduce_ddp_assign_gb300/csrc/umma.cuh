@@ -44,6 +44,11 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t b)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
 }
+// 16 bytes of another CTA's shared memory (address in the cluster's shared memory)
+__device__ __forceinline__ void store_cluster(uint32_t a, int4 v)
+{
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity)
 {
     uint32_t done;

@@ -24,6 +24,8 @@ namespace {
 
 constexpr int kRowTile = 256;   // rows of the gathered arrays are padded to this
 constexpr int kPrepThreads = 256;
+// G of one piece of the vocabulary, times two: 2^26 elements are 134 MB each
+constexpr int64_t kPieceElements = int64_t{1} << 26;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // G's scale in fp16: its largest magnitude, 1 after the division by the largest
@@ -31,9 +33,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 // numbers.  bf16 has fp32's exponents and needs none.
 template <int DT> constexpr float g_scale() { return DT == DDP_F16 ? 16384.f : 1.f; }
 
+// dH's tiles are split along the vocabulary while there are fewer than this many
+// of them, about one for each pair of SMs (by a constant, so that the order of its sums
+// does not depend on the device).
+constexpr int kSplitTiles = 76;
+__host__ __device__ __forceinline__ int dh_splits(int mt, int nt, int nkb)
+{
+    const int want = (kSplitTiles + mt * nt - 1) / (mt * nt), most = (nkb + 7) / 8;
+    return want < most ? want : most;
+}
+
 struct Space {
-    int64_t count, gmax, rows, target, ratio, lse, hidden, part, ztarget, grad, acc, weight, total;
-    int64_t piece, ntiles, tpad, dpad;
+    int64_t count, gmax, next, rows, target, ratio, lse, hidden, part, ztarget, grad, acc, weight, total;
+    int64_t piece, pieces, ntiles, tpad, dpad, grad_bytes;
 };
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -45,8 +57,9 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     s.dpad = round_up(D, 8);
     s.ntiles = (V + 127) / 128;  // one pair of statistics a row for each 128 words
     const int64_t vpad = round_up(V, 256);
-    if (piece <= 0) piece = std::max<int64_t>(1024, (int64_t{1} << 27) / s.tpad);
+    if (piece <= 0) piece = std::max<int64_t>(1024, kPieceElements / s.tpad);
     s.piece = std::min(vpad, round_up(piece, 256));
+    s.pieces = backward ? (V + s.piece - 1) / s.piece : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t p = at;
@@ -55,14 +68,18 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     };
     s.count = take(4);
     s.gmax = take(4);
+    s.next = take(4 * (s.pieces + 1));
     s.rows = take(4 * s.tpad);
     s.target = take(4 * s.tpad);
     s.hidden = take(2 * s.tpad * s.dpad);
     if (backward) {
         s.ratio = take(4 * s.tpad);
         s.lse = take(4 * s.tpad);
-        s.grad = take(2 * s.tpad * s.piece);
-        s.acc = take(s.piece < vpad ? 4 * s.tpad * s.dpad : 0);
+        s.grad_bytes = round_up(2 * s.tpad * s.piece, 256);
+        s.grad = take(s.grad_bytes * std::min<int64_t>(s.pieces, 2));  // one is filled while the other is read
+        // splits x rows: at most (kSplitTiles / nt + mt) tiles of rows
+        const int64_t nt = (D + 255) / 256;
+        s.acc = take(4 * s.dpad * (s.tpad + kRowTile * ((kSplitTiles + nt - 1) / nt)));
     } else {
         s.part = take(8 * s.tpad * s.ntiles);
         s.ztarget = take(4 * s.tpad);
@@ -102,6 +119,9 @@ struct PrepArgs {
     uint16_t* gh;         // rows to clear
     int64_t ghs;
     float g_scale;
+    int32_t vec;          // hidden (and gh) in 16-byte vectors
+    int32_t* next;        // tile counters of the launches that follow
+    int32_t nnext;
 };
 
 __device__ __forceinline__ bool token_target(const PrepArgs& a, int t, int64_t* y)
@@ -134,16 +154,28 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
     __shared__ int place[kPrepThreads];  // of the slab's tokens: gathered row or -1
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = blockIdx.x * a.slab, t1 = min(a.T, t0 + a.slab);
+    wait_for_previous();
+    if (blockIdx.x == 0)
+        for (int i = tid; i < a.nnext; i += kPrepThreads) a.next[i] = 0;
     int before = 0, all = 0;
     float gm = 0.f;
-    for (int t = tid; t < a.T; t += kPrepThreads) {
-        int64_t y;
-        if (!token_target(a, t, &y)) continue;
-        ++all;
-        before += t < t0;
-        if (a.gl) {
-            const float g = fabsf(a.gl[static_cast<int64_t>(t) * a.gl_stride]);
-            if (g > gm && g <= 3.4028234663852886e38f) gm = g;
+    // eight tokens a thread at a time, their loads in flight together
+    for (int t = tid; t < a.T; t += 8 * kPrepThreads) {
+        int64_t y[8];
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int u = t + j * kPrepThreads;
+            y[j] = u < a.T ? load_id(a.targets, a.id_bytes, u) : a.ignore;
+            g[j] = a.gl && u < a.T ? a.gl[static_cast<int64_t>(u) * a.gl_stride] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (y[j] == a.ignore || y[j] < 0 || y[j] >= a.vocab) continue;
+            ++all;
+            before += t + j * kPrepThreads < t0;
+            const float x = fabsf(g[j]);
+            if (x > gm && x <= 3.4028234663852886e38f) gm = x;
         }
     }
     before = block_sum(before, sh);
@@ -181,26 +213,42 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
         }
     }
     __syncthreads();
-    for (int i = warp; i < t1 - t0; i += kPrepThreads / 32) {
-        const int at = place[i];
-        const uint16_t* src = static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + i) * a.hs;
-        if (at >= 0) {
-            uint16_t* dst = a.out + static_cast<int64_t>(at) * a.dpad;
-            for (int64_t c = lane; c < a.dpad; c += 32) dst[c] = c < a.dim ? src[c] : 0;
-        } else if (a.gh) {
-            uint16_t* dst = a.gh + static_cast<int64_t>(t0 + i) * a.ghs;
-            for (int64_t c = lane; c < a.dim; c += 32) dst[c] = 0;
+    // rows in 16-byte vectors where the tensors allow it
+    const int64_t vecs = a.vec ? a.dpad / 8 : 0;
+    for (int64_t i = tid; i < vecs * (t1 - t0); i += kPrepThreads) {
+        const int r = static_cast<int>(i / vecs);
+        const int64_t c = (i - r * vecs) * 8;
+        const int at = place[r];
+        if (at >= 0)
+            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(at) * a.dpad + c) =
+                *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs + c);
+        else if (a.gh)
+            *reinterpret_cast<uint4*>(a.gh + static_cast<int64_t>(t0 + r) * a.ghs + c) = make_uint4(0, 0, 0, 0);
+    }
+    if (!a.vec) {
+        for (int i = warp; i < t1 - t0; i += kPrepThreads / 32) {
+            const int at = place[i];
+            const uint16_t* src = static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + i) * a.hs;
+            if (at >= 0) {
+                uint16_t* dst = a.out + static_cast<int64_t>(at) * a.dpad;
+                for (int64_t c = lane; c < a.dpad; c += 32) dst[c] = c < a.dim ? src[c] : 0;
+            } else if (a.gh) {
+                uint16_t* dst = a.gh + static_cast<int64_t>(t0 + i) * a.ghs;
+                for (int64_t c = lane; c < a.dim; c += 32) dst[c] = 0;
+            }
         }
     }
     // rows up to the tile's end are zeros (past the T-th the copies supply them): they are terms of dW's sums
     const int end = min(a.T, (all + kRowTile - 1) / kRowTile * kRowTile);
     for (int r = all + blockIdx.x; r < end; r += gridDim.x)
-        for (int64_t c = tid; c < a.dpad; c += kPrepThreads) a.out[static_cast<int64_t>(r) * a.dpad + c] = 0;
+        for (int64_t c = tid * 8; c < a.dpad; c += kPrepThreads * 8)
+            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(r) * a.dpad + c) = make_uint4(0, 0, 0, 0);
 }
 
 __global__ void __launch_bounds__(256)
 copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, uint16_t* out, int64_t dpad)
 {
+    wait_for_previous();
     for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x)
         for (int64_t c = threadIdx.x; c < dpad; c += blockDim.x) out[v * dpad + c] = c < dim ? w[v * ws + c] : 0;
 }
@@ -213,9 +261,12 @@ copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, ui
 // thread of the first CTA issues the products of both.  Per CTA:
 //   warp 8     copies 128 x 64 boxes of A and B into a ring of stages;
 //   warp 9     (first CTA) issues four k = 16 products a stage;
+//   warp 10    (first CTA) claims tiles from a counter and passes them to both CTAs;
 //   warps 0-7  take finished tiles out of tensor memory, which holds two, so that
 //              a tile's epilogue runs under the next tile's products.
-// The grid is one pair of CTAs for each pair of SMs; a pair takes every npairs-th tile.
+// A launch runs up to three products, their tiles one after the other, longest
+// first: with dH and dW of one piece of the vocabulary comes G of the next, whose
+// short tiles fill what the long ones leave idle at the end.
 enum Use { USE_STATS, USE_GRAD, USE_DH, USE_DW };
 
 constexpr int kTile = 256;               // rows and columns of a pair's tile
@@ -226,17 +277,20 @@ constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kStagingBytes = 4096;      // per epilogue warp: 32 rows of 128 bytes
-constexpr int kProductThreads = 32 * (kEpiWarps + 2);
+constexpr int kSlots = 4;                // claimed tiles on their way to the warps
+constexpr int kProductThreads = 32 * (kEpiWarps + 3);
 constexpr int kProductSmem = kStages * kStageBytes + kEpiWarps * kStagingBytes + 1024;
+constexpr int kGroup = 32;               // tiles along the fast side before the slow side moves on
+constexpr int kMaxJobs = 3;
 
 struct Product {
     CUtensorMap ta, tb;
+    int32_t use;
+    int32_t a_mn, b_mn;   // the operand's rows (not k) are contiguous in memory
     int64_t M, N, K;
-    const int32_t* count; // gathered rows: bounds M (STATS, GRAD, DH) or K (DW)
     int64_t rows_cap;     // rows of the gathered arrays that exist
     int64_t v0;           // first word of the piece
     const int32_t* target;
-    int* status;
     // STATS
     float2* part;
     int64_t tpad;
@@ -249,34 +303,86 @@ struct Product {
     // DH, DW
     const float* gmax;
     float inv_scale;
-    float* acc;           // fp32 sums over the pieces (nullptr: one piece)
+    float* acc;           // dH: fp32 sums over pieces and splits, [split][row][ald]
+    int64_t ald;
     int32_t first, last;
     const int32_t* rows;
     void* out;
     int64_t os;
     int32_t out_f32, accumulate, vec;
 };
-
-template <int USE> struct Majors {
-    static constexpr bool a_mn = USE == USE_DW;
-    static constexpr bool b_mn = USE == USE_DH || USE == USE_DW;
+struct Batch {
+    Product job[kMaxJobs];
+    int32_t njobs;
+    const int32_t* count; // gathered rows: bounds M (STATS, GRAD, DH) or K (DW)
+    int32_t* next;        // tiles claimed beyond each pair's first
+    int* status;
 };
 
-// one CTA's 128 rows of an operand, 64 of k: one box, or two where m (n) is contiguous
-template <bool MN>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int k, uint32_t bar)
+// What a launch's warps know of a product: its tiles, and how many there are.
+struct Shape {
+    int32_t mt, nt, nkb, splits;
+    int64_t M, tiles;
+};
+__device__ __forceinline__ Shape shape_of(const Product& p, int64_t count)
 {
-    if (MN) {
+    Shape s;
+    const int64_t K = p.use == USE_DW ? min(p.K, count) : p.K;
+    s.M = p.use == USE_DW ? p.M : min(p.M, count);
+    s.mt = static_cast<int>((s.M + kTile - 1) / kTile);
+    s.nt = static_cast<int>((p.N + kTile - 1) / kTile);
+    s.nkb = static_cast<int>((K + kBlockK - 1) / kBlockK);
+    // (the splits follow from the whole product's length, not this piece's: the sums' layout is the same for every piece)
+    s.splits = p.use == USE_DH && s.mt > 0 ? dh_splits(s.mt, s.nt, static_cast<int>((p.gld + kBlockK - 1) / kBlockK)) : 1;
+    s.tiles = static_cast<int64_t>(s.mt) * s.nt * s.splits;
+    return s;
+}
+struct Tile {
+    int32_t job, m, n, split, kb0, kb1;  // job < 0: no more tiles
+    int32_t pad_[2];
+};
+// Tile t of a launch.  Tiles that run at the same time share operands: up to kGroup
+// along the side whose operand is the smaller one (the hidden states), then a
+// step along the other, so that the larger one is read from HBM once.
+__device__ __forceinline__ Tile tile_at(int64_t t, const Batch& b, const Shape* shapes)
+{
+    Tile r{};
+    while (r.job + 1 < b.njobs && t >= shapes[r.job].tiles) t -= shapes[r.job++].tiles;
+    const Shape& s = shapes[r.job];
+    const int64_t mn = static_cast<int64_t>(s.mt) * s.nt;
+    r.split = static_cast<int>(t / mn);
+    t -= r.split * mn;
+    const bool n_fast = b.job[r.job].use == USE_DW;
+    const int fast = n_fast ? s.nt : s.mt, slow = n_fast ? s.mt : s.nt;
+    const int group = static_cast<int>(t / (static_cast<int64_t>(kGroup) * slow));
+    const int64_t in = t - static_cast<int64_t>(group) * kGroup * slow;
+    const int width = min(kGroup, fast - group * kGroup);
+    const int i = group * kGroup + static_cast<int>(in % width), o = static_cast<int>(in / width);
+    r.m = n_fast ? o : i;
+    r.n = n_fast ? i : o;
+    const int per = (s.nkb + s.splits - 1) / s.splits;
+    r.kb0 = min(s.nkb, r.split * per);
+    r.kb1 = min(s.nkb, r.kb0 + per);
+    return r;
+}
+
+// one CTA's 128 rows of an operand, 64 of k: one box, or two where the rows are contiguous
+__device__ __forceinline__ void load_operand(bool mn, uint32_t dst, const CUtensorMap* map, int row, int k, uint32_t bar)
+{
+    if (mn) {
         tensor_load(dst, map, row, k, bar);
         tensor_load(dst + kOperandBytes / 2, map, row + 64, k, bar);
     } else {
         tensor_load(dst, map, k, row, bar);
     }
 }
-// descriptor of k = 16 values at step j of a stage
-template <bool MN> __device__ __forceinline__ uint64_t step_desc(uint32_t base, int j)
+
+// 2^x; results below 2^-126 are zero: no probability that small adds to a sum of 1
+__device__ __forceinline__ float pow2(float x)
 {
-    return MN ? operand_desc(base + j * 2048, kOperandBytes / 2, 1024) : operand_desc(base + j * 32, 16, 1024);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ void tile_values(uint32_t taddr, bool empty, float (&c)[32])
@@ -312,10 +418,11 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b)
 }
 
 template <int DT, int USE>
-__device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool empty, int64_t m0, int64_t n0, int64_t M,
-                                         uint32_t staging, int half, int lane)
+__device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, const Tile& tile, uint32_t taddr, bool empty,
+                                         int64_t m0, int64_t n0, uint32_t staging, int lane)
 {
     using T = typename Elem<DT>::T;
+    const int64_t M = shape.M;
     const int64_t m = m0 + lane;  // this thread's row; n0: the warp's first of 128 columns
     float c[32];
     if (USE == USE_STATS) {
@@ -342,12 +449,12 @@ __device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool 
             const float top = fmaxf(mx, cm);
             if (top != -INFINITY) {  // all of them minus infinity: they add nothing
                 const float shift = top * kLog2e;
-                s *= mx == -INFINITY ? 0.f : exp2f(mx * kLog2e - shift);
+                s *= mx == -INFINITY ? 0.f : pow2(mx * kLog2e - shift);
                 float a0 = 0.f, a1 = 0.f;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    a0 += exp2f(fmaf(c[j], kLog2e, -shift));
-                    a1 += exp2f(fmaf(c[j + 1], kLog2e, -shift));
+                    a0 += pow2(fmaf(c[j], kLog2e, -shift));
+                    a1 += pow2(fmaf(c[j + 1], kLog2e, -shift));
                 }
                 s += a0 + a1;
                 mx = top;
@@ -367,7 +474,7 @@ __device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool 
                 const int64_t n = n0 + q * 64 + h * 32;
                 tile_values(taddr + q * 64 + h * 32, empty, c);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) c[j] = exp2f(fmaf(c[j], kLog2e, -shift));
+                for (int j = 0; j < 32; ++j) c[j] = pow2(fmaf(c[j], kLog2e, -shift));
                 if (y >= n && y < n + 32) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) c[j] -= y - n == j ? 1.f : 0.f;
@@ -396,6 +503,10 @@ __device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool 
         }
     } else {
         const float alpha = *p.gmax * p.inv_scale;
+        // dH of one piece without splits needs no sums in memory
+        const bool sums = USE == USE_DH && !(p.first && p.last && shape.splits == 1);
+        const bool result = USE != USE_DH || (p.last && shape.splits == 1);
+        float* acc = p.acc + static_cast<int64_t>(tile.split) * shape.mt * kTile * p.ald;
         for (int q = 0; q < 4; ++q) {
             tile_values(taddr + q * 32, empty, c);
             if (n0 + q * 32 >= p.N) break;
@@ -413,13 +524,13 @@ __device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool 
                 const int64_t row = m0 + r;
                 if (row >= M || n >= p.N) continue;
                 const int width = static_cast<int>(min(static_cast<int64_t>(4), p.N - n));
-                if (USE == USE_DH && p.acc) {
-                    float* a = p.acc + row * p.tpad + n;  // tpad: the sums' row stride, a multiple of 4
+                if (sums) {
+                    float* a = acc + row * p.ald + n;  // ald is a multiple of 8
                     if (!p.first) {
                         const float4 o = *reinterpret_cast<const float4*>(a);
                         x[0] += o.x; x[1] += o.y; x[2] += o.z; x[3] += o.w;
                     }
-                    if (!p.last) {
+                    if (!result) {
                         *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]);
                         continue;
                     }
@@ -459,12 +570,41 @@ __device__ __forceinline__ void epilogue(const Product& p, uint32_t taddr, bool 
     }
 }
 
-template <int DT, int USE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product p)
+// One thread issues a tile's products, `it` stages into the ring.  It has the time of
+// four products (about 500 cycles) for each stage, so nothing but additions of
+// constants is left in the loop.
+template <int DT, bool A_MN, bool B_MN>
+__device__ __forceinline__ bool issue_products(uint32_t d, int blocks, uint32_t it, uint32_t base, uint32_t bar0, volatile int* dead)
+{
+    constexpr uint32_t desc = product_desc(DT == DDP_BF16, A_MN, B_MN, kTile, kTile);
+    // rows contiguous: 8 k (1024 bytes) after 8 k, blocks of 64 rows apart; k contiguous: 16 k are 32 bytes
+    constexpr uint64_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
+    const uint64_t a0 = operand_desc(base, A_MN ? kOperandBytes / 2 : 16, 1024);
+    const uint64_t b0 = operand_desc(base + kOperandBytes, B_MN ? kOperandBytes / 2 : 16, 1024);
+    uint32_t s = it % kStages, parity = (it / kStages) & 1;
+    for (int kb = 0; kb < blocks; ++kb) {
+        if (!bar_wait(bar0 + 8u * s, parity, dead)) return false;
+        tmem_fence_after();
+        const uint64_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < kBlockK / 16; ++k) product_pair(d, a + k * a_step, b + k * b_step, desc, kb > 0 || k > 0);
+        product_commit(bar0 + 8u * (kStages + s));
+        if (++s == kStages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+    return true;
+}
+
+template <int DT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Batch batch)
 {
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kSlots];
+    __shared__ Shape shapes[kMaxJobs];
     __shared__ uint32_t tmem_base;
+    __shared__ __align__(16) Tile slot_tile[kSlots];
     __shared__ volatile int dead;
     const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_addr(bars);
@@ -474,6 +614,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
     auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
     auto tfull = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
     auto tempty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+    auto sfull = [&](int i) { return bar0 + 8u * (2 * kStages + 4 + i); };
+    auto sempty = [&](int i) { return bar0 + 8u * (2 * kStages + 4 + kSlots + i); };
 
     if (threadIdx.x == 0) {
         dead = 0;
@@ -485,95 +627,149 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
             bar_init(tfull(b), 1);
             bar_init(tempty(b), 2 * kEpiWarps);
         }
+        for (int i = 0; i < kSlots; ++i) {
+            bar_init(sfull(i), 1);
+            bar_init(sempty(i), 2 * kEpiWarps + 3);  // both CTAs' epilogue and copy warps, the product warp
+        }
         bar_init_fence();
-        tensor_map_prefetch(&p.ta);
-        tensor_map_prefetch(&p.tb);
+        for (int i = 0; i < batch.njobs; ++i) {
+            tensor_map_prefetch(&batch.job[i].ta);
+            tensor_map_prefetch(&batch.job[i].tb);
+        }
     }
     if (warp == 9) tmem_alloc(smem_addr(&tmem_base), 512);
+    wait_for_previous();
+    if (threadIdx.x < batch.njobs) shapes[threadIdx.x] = shape_of(batch.job[threadIdx.x], *batch.count);
     tmem_fence_before();
     __syncthreads();
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
 
-    const int64_t count = *p.count;
-    const int64_t M = USE == USE_DW ? p.M : min(p.M, count);
-    const int64_t K = USE == USE_DW ? min(p.K, count) : p.K;
-    const int mt = static_cast<int>((M + kTile - 1) / kTile), nt = static_cast<int>((p.N + kTile - 1) / kTile);
-    const int nkb = static_cast<int>((K + kBlockK - 1) / kBlockK);
-    const int64_t tiles = static_cast<int64_t>(mt) * nt;
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    // the i-th tile of this pair; every warp that asks releases the slot
+    auto next_tile = [&](uint32_t i, Tile* t) {
+        const int s = i % kSlots;
+        const bool ok = bar_wait(sfull(s), (i / kSlots) & 1, &dead);
+        const uint4 lo = lds16(smem_addr(&slot_tile[s])), hi = lds16(smem_addr(&slot_tile[s]) + 16);
+        t->job = lo.x; t->m = lo.y; t->n = lo.z; t->split = lo.w;
+        t->kb0 = hi.x; t->kb1 = hi.y;
+        return ok;
+    };
+    auto release_slot = [&](uint32_t i) { bar_arrive_cluster(cluster_addr(sempty(i % kSlots), 0)); };
 
-    if (warp == 8) {
-        if (lane == 0 && nkb > 0) {
+    if (warp == 10) {
+        // claims and works out tiles a few ahead of the warps that use them: the copies and
+        // the products stand still for as long as their threads think
+        if (rank == 0 && lane == 0) {
+            int64_t total = 0;
+            for (int i = 0; i < batch.njobs; ++i) total += shapes[i].tiles;
+            const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+            for (uint32_t i = 0;; ++i) {
+                const int s = i % kSlots;
+                const int64_t t = i == 0 ? pair : npairs + static_cast<int64_t>(atomicAdd(batch.next, 1));
+                Tile x{};
+                if (t < total) x = tile_at(t, batch, shapes);
+                else x.job = -1;
+                if (!bar_wait(sempty(s), ((i / kSlots) & 1) ^ 1, &dead)) break;
+                for (uint32_t r = 0; r < 2; ++r) {
+                    const uint32_t at = cluster_addr(smem_addr(&slot_tile[s]), r);
+                    store_cluster(at, make_int4(x.job, x.m, x.n, x.split));
+                    store_cluster(at + 16, make_int4(x.kb0, x.kb1, 0, 0));
+                    bar_arrive_cluster(cluster_addr(sfull(s), r));
+                }
+                if (x.job < 0) break;
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t t = pair; ok && t < tiles; t += npairs) {
-                const int m = static_cast<int>(t % mt) * kTile + static_cast<int>(rank) * kHalf;
-                const int n = static_cast<int>(t / mt) * kTile + static_cast<int>(rank) * kHalf;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!(ok = bar_wait(empty(s), ((it / kStages) & 1) ^ 1, &dead))) break;
+            for (uint32_t i = 0; ok; ++i) {
+                Tile x;
+                if (!(ok = next_tile(i, &x))) break;
+                release_slot(i);
+                if (x.job < 0) break;
+                const Product& p = batch.job[x.job];
+                const int m = x.m * kTile + static_cast<int>(rank) * kHalf, n = x.n * kTile + static_cast<int>(rank) * kHalf;
+                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                const uint32_t lead = cluster_addr(bar0, 0);
+                uint32_t s = it % kStages, parity = ((it / kStages) & 1) ^ 1;
+                for (int kb = x.kb0; kb < x.kb1; ++kb, ++it) {
+                    if (!(ok = bar_wait(empty(s), parity, &dead))) break;
                     // both CTAs' bytes are counted on the first CTA's barrier
                     if (rank == 0) bar_expect(full(s), 2 * kStageBytes);
-                    const uint32_t bar = cluster_addr(full(s), 0);
+                    const uint32_t bar = lead + 8u * s;
                     const uint32_t a = base + s * kStageBytes;
-                    load_operand<Majors<USE>::a_mn>(a, &p.ta, m, kb * kBlockK, bar);
-                    load_operand<Majors<USE>::b_mn>(a + kOperandBytes, &p.tb, n, kb * kBlockK, bar);
+                    load_operand(a_mn, a, &p.ta, m, kb * kBlockK, bar);
+                    load_operand(b_mn, a + kOperandBytes, &p.tb, n, kb * kBlockK, bar);
+                    if (++s == kStages) {
+                        s = 0;
+                        parity ^= 1;
+                    }
                 }
             }
             // the last arrivals on this CTA's barriers come before it may leave
             for (int i = 0; ok && i < kStages; ++i, ++it) ok = bar_wait(empty(it % kStages), ((it / kStages) & 1) ^ 1, &dead);
         }
     } else if (warp == 9) {
-        if (rank == 0 && lane == 0 && nkb > 0) {
-            constexpr uint32_t desc = product_desc(DT == DDP_BF16, Majors<USE>::a_mn, Majors<USE>::b_mn, kTile, kTile);
+        if (rank == 0 && lane == 0) {
             uint32_t it = 0, j = 0;
             bool ok = true;
-            for (int64_t t = pair; ok && t < tiles; t += npairs, ++j) {
+            for (uint32_t i = 0; ok; ++i) {
+                Tile x;
+                if (!(ok = next_tile(i, &x))) break;
+                release_slot(i);
+                if (x.job < 0) break;
+                if (x.kb0 == x.kb1) continue;
+                const Product& p = batch.job[x.job];
                 const int b = j & 1;
                 if (!(ok = bar_wait(tempty(b), ((j >> 1) & 1) ^ 1, &dead))) break;
                 tmem_fence_after();
                 const uint32_t d = tmem + b * kTile;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!(ok = bar_wait(full(s), (it / kStages) & 1, &dead))) break;
-                    tmem_fence_after();
-                    const uint32_t a = base + s * kStageBytes;
-#pragma unroll
-                    for (int k = 0; k < kBlockK / 16; ++k)
-                        product_pair(d, step_desc<Majors<USE>::a_mn>(a, k), step_desc<Majors<USE>::b_mn>(a + kOperandBytes, k),
-                                     desc, kb > 0 || k > 0);
-                    product_commit(empty(s));
-                }
+                const int blocks = x.kb1 - x.kb0;
+                if (p.b_mn == 0) ok = issue_products<DT, false, false>(d, blocks, it, base, bar0, &dead);
+                else if (p.a_mn == 0) ok = issue_products<DT, false, true>(d, blocks, it, base, bar0, &dead);
+                else ok = issue_products<DT, true, true>(d, blocks, it, base, bar0, &dead);
+                it += blocks;
                 if (ok) product_commit(tfull(b));
+                ++j;
             }
         }
     } else {
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t staging = base + kStages * kStageBytes + warp * kStagingBytes;
         uint32_t j = 0;
-        for (int64_t t = pair; t < tiles; t += npairs, ++j) {
+        for (uint32_t i = 0;; ++i) {
+            Tile x;
+            if (!__all_sync(0xffffffffu, next_tile(i, &x))) break;
+            if (lane == 0) release_slot(i);
+            if (x.job < 0) break;
+            const Product& p = batch.job[x.job];
+            const bool none = x.kb0 == x.kb1;
             const int b = j & 1;
-            if (nkb > 0) {
+            if (!none) {
                 if (!__all_sync(0xffffffffu, bar_wait(tfull(b), (j >> 1) & 1, &dead))) break;
                 tmem_fence_after();
+                ++j;
             }
-            const int64_t m0 = (t % mt) * kTile + rank * kHalf + quarter * 32;
-            const int64_t n0 = (t / mt) * kTile + half * kHalf;
-            __syncwarp();
-            epilogue<DT, USE>(p, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * kTile + half * kHalf, nkb == 0, m0,
-                              n0, M, staging, half, lane);
+            const int64_t m0 = static_cast<int64_t>(x.m) * kTile + rank * kHalf + quarter * 32;
+            const int64_t n0 = static_cast<int64_t>(x.n) * kTile + half * kHalf;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * kTile + half * kHalf;
+            const Shape& sh = shapes[x.job];
+            if (p.use == USE_STATS) epilogue<DT, USE_STATS>(p, sh, x, taddr, none, m0, n0, staging, lane);
+            else if (p.use == USE_GRAD) epilogue<DT, USE_GRAD>(p, sh, x, taddr, none, m0, n0, staging, lane);
+            else if (p.use == USE_DH) epilogue<DT, USE_DH>(p, sh, x, taddr, none, m0, n0, staging, lane);
+            else epilogue<DT, USE_DW>(p, sh, x, taddr, none, m0, n0, staging, lane);
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0 && nkb > 0) bar_arrive_cluster(cluster_addr(tempty(b), 0));
+            if (lane == 0 && !none) bar_arrive_cluster(cluster_addr(tempty(b), 0));
         }
     }
     __syncthreads();
     if (dead) {
         // a wait gave up: report it, and let copies and products in flight end before the memory is given back
         if (threadIdx.x == 0) {
-            atomicOr(p.status, kErrWait);
+            atomicOr(batch.status, kErrWait);
             const uint64_t t0 = clock_ns();
             for (uint32_t i = 0; i < (1u << 24) && clock_ns() - t0 < 20000000ull; ++i) {}
         }
@@ -583,6 +779,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
     cluster_sync();
     tmem_fence_after();
     if (warp == 9) tmem_free(tmem, 512);
+}
+
+// dH where its tiles were split along the vocabulary: the splits' sums, in order
+template <int DT>
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Product p, const int32_t* count)
+{
+    using T = typename Elem<DT>::T;
+    wait_for_previous();
+    const Shape sh = shape_of(p, *count);
+    if (sh.splits == 1) return;
+    const float alpha = *p.gmax * p.inv_scale;
+    const int64_t quads = p.ald / 4, size = static_cast<int64_t>(sh.mt) * kTile * p.ald;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < sh.M * quads; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = i / quads, n = (i - row * quads) * 4;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < sh.splits; ++s) {
+            const float4 v = *reinterpret_cast<const float4*>(p.acc + s * size + row * p.ald + n);
+            x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
+        }
+        T* o = static_cast<T*>(p.out) + p.rows[row] * p.os + n;
+        if (p.vec && n + 4 <= p.N) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(pack2<DT>(x[0] * alpha, x[1] * alpha), pack2<DT>(x[2] * alpha, x[3] * alpha));
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (n + j < p.N) o[j] = Elem<DT>::from_f(x[j] * alpha);
+        }
+    }
 }
 
 // A matrix of 16-bit values, `inner` contiguous values a row, cut in boxes of 64 values by `box_rows` rows.
@@ -618,38 +842,51 @@ bool make_map(CUtensorMap* map, int dtype, const void* ptr, int64_t inner, int64
 }
 
 // the operands' maps: A is [M x K] and B [N x K] seen as stored, `*_stride` between stored rows
-template <int DT, int USE>
-cudaError_t launch_product(Product& p, const void* a, int64_t a_stride, const void* b, int64_t b_stride, cudaStream_t s)
+bool set_operands(Product& p, int dtype, int use, const void* a, int64_t a_stride, const void* b, int64_t b_stride)
+{
+    p.use = use;
+    p.a_mn = use == USE_DW;
+    p.b_mn = use == USE_DH || use == USE_DW;
+    return (p.a_mn ? make_map(&p.ta, dtype, a, p.M, p.K, a_stride, kBlockK) : make_map(&p.ta, dtype, a, p.K, p.M, a_stride, kHalf)) &&
+           (p.b_mn ? make_map(&p.tb, dtype, b, p.N, p.K, b_stride, kBlockK) : make_map(&p.tb, dtype, b, p.K, p.N, b_stride, kHalf));
+}
+
+template <int DT> cudaError_t launch_products(const Batch& batch, cudaStream_t s)
 {
     static std::atomic<int> cached[ddp::kMaxDevices] = {};
-    if (Majors<USE>::a_mn ? !make_map(&p.ta, DT, a, p.M, p.K, a_stride, kBlockK) : !make_map(&p.ta, DT, a, p.K, p.M, a_stride, kHalf))
-        return cudaErrorInvalidValue;
-    if (Majors<USE>::b_mn ? !make_map(&p.tb, DT, b, p.N, p.K, b_stride, kBlockK) : !make_map(&p.tb, DT, b, p.K, p.N, b_stride, kHalf))
-        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = kProductSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     const int dev = ddp::current_device();
     int pairs = dev >= 0 ? cached[dev].load(std::memory_order_relaxed) : 0;
     if (!pairs) {
-        cudaError_t e = cudaFuncSetAttribute(product_kernel<DT, USE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+        cudaError_t e = cudaFuncSetAttribute(product_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
         if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kProductThreads);
-        cfg.dynamicSmemBytes = kProductSmem;
-        cudaLaunchAttribute at{};
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = 2;
-        at.val.clusterDim.y = at.val.clusterDim.z = 1;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&pairs, product_kernel<DT, USE>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&pairs, product_kernel<DT>, &cfg);
         if (e != cudaSuccess) return e;
         pairs = std::max(1, std::min(pairs, ddp::device_sm_count() / 2));
         if (dev >= 0) cached[dev].store(pairs, std::memory_order_relaxed);
     }
-    const int64_t tiles = ((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
-    const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, pairs));
-    product_kernel<DT, USE><<<grid, kProductThreads, kProductSmem, s>>>(p);
-    return cudaGetLastError();
+    int64_t tiles = 0;
+    for (int i = 0; i < batch.njobs; ++i) {
+        const Product& p = batch.job[i];
+        const int64_t mt = (p.M + kTile - 1) / kTile, nt = (p.N + kTile - 1) / kTile;
+        tiles += mt * nt;
+        if (p.use == USE_DH) tiles += kSplitTiles;  // fewer rows on the device may mean more splits
+    }
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
+    // the cluster's size is the kernel's own; it may start while the kernel before it ends
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, product_kernel<DT>, batch);
 }
 
 // joins the (maximum, sum) pairs of each gathered row: 32 threads a row, in a fixed order
@@ -675,6 +912,7 @@ combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, in
     using T = typename Elem<DT>::T;
     __shared__ float2 sh[32][kJoinRows];
     __shared__ float dot[32][kJoinRows];
+    wait_for_previous();
     const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
     const int64_t m = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
     const bool in = m < *count;
@@ -749,7 +987,7 @@ ddp_status check(const char* fn, const Call& c, const void* workspace, int64_t w
 bool needs_copy(const Call& c) { return !aligned16(c.weight) || c.ws % 8 != 0; }
 
 // gathers, and the weight's aligned copy where it needs one
-void launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, int* status, cudaStream_t s, const void** weight, int64_t* ws)
+cudaError_t launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, int* status, cudaStream_t s, const void** weight, int64_t* ws)
 {
     a.hidden = c.hidden;
     a.hs = c.hs;
@@ -766,16 +1004,21 @@ void launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, int* stat
     a.target = reinterpret_cast<int32_t*>(w + sp.target);
     a.out = reinterpret_cast<uint16_t*>(w + sp.hidden);
     a.status = status;
-    prep_kernel<<<static_cast<unsigned>((c.T + a.slab - 1) / a.slab), kPrepThreads, 0, s>>>(a);
+    a.vec = c.D % 8 == 0 && c.hs % 8 == 0 && aligned16(c.hidden) && (!a.gh || (aligned16(a.gh) && a.ghs % 8 == 0));
+    a.next = reinterpret_cast<int32_t*>(w + sp.next);
+    a.nnext = static_cast<int32_t>(sp.pieces + 1);
+    cudaError_t e = launch_chained(prep_kernel, dim3(static_cast<unsigned>((c.T + a.slab - 1) / a.slab)), kPrepThreads, 0, s, a);
+    if (e != cudaSuccess) return e;
     *weight = c.weight;
     *ws = c.ws;
     if (needs_copy(c)) {
         uint16_t* dst = reinterpret_cast<uint16_t*>(w + sp.weight);
-        copy_weight_kernel<<<static_cast<unsigned>(std::min<int64_t>(c.V, 1 << 20)), 256, 0, s>>>(
-            static_cast<const uint16_t*>(c.weight), c.ws, c.V, c.D, dst, sp.dpad);
+        e = launch_chained(copy_weight_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(c.V, 1 << 20))), 256, 0, s,
+                           static_cast<const uint16_t*>(c.weight), c.ws, c.V, c.D, dst, sp.dpad);
         *weight = dst;
         *ws = sp.dpad;
     }
+    return e;
 }
 
 template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* w, int* status, float* loss, float* lse, cudaStream_t s)
@@ -785,21 +1028,27 @@ template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* 
     a.lse_out = lse;
     const void* weight;
     int64_t ws;
-    launch_prep(a, c, sp, w, status, s, &weight, &ws);
-    Product p{};
+    cudaError_t e = launch_prep(a, c, sp, w, status, s, &weight, &ws);
+    if (e != cudaSuccess) return e;
+    Batch batch{};
+    batch.njobs = 1;
+    batch.count = a.count;
+    batch.next = a.next;
+    batch.status = status;
+    Product& p = batch.job[0];
     p.M = c.T; p.N = c.V; p.K = c.D;
-    p.count = a.count;
     p.target = a.target;
-    p.status = status;
     p.part = reinterpret_cast<float2*>(w + sp.part);
     p.tpad = sp.tpad;
     p.ztarget = reinterpret_cast<float*>(w + sp.ztarget);
-    const cudaError_t e = launch_product<DT, USE_STATS>(p, a.out, sp.dpad, weight, ws, s);
+    if (!set_operands(p, DT, USE_STATS, a.out, sp.dpad, weight, ws)) return cudaErrorInvalidValue;
+    e = launch_products<DT>(batch, s);
     if (e != cudaSuccess) return e;
-    combine_kernel<DT><<<static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows), 32 * kJoinRows, 0, s>>>(
-        a.count, a.rows, p.part, sp.tpad, static_cast<int>(sp.ntiles), p.ztarget, a.out, sp.dpad, weight, ws, c.D, a.target,
-        loss, lse);
-    return cudaGetLastError();
+    return launch_chained(combine_kernel<DT>, dim3(static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows)), 32 * kJoinRows, 0, s,
+                          static_cast<const int32_t*>(a.count), static_cast<const int32_t*>(a.rows),
+                          static_cast<const float2*>(p.part), sp.tpad, static_cast<int>(sp.ntiles),
+                          static_cast<const float*>(p.ztarget), static_cast<const void*>(a.out), sp.dpad, weight, ws, c.D,
+                          static_cast<const int32_t*>(a.target), loss, lse);
 }
 
 template <int DT>
@@ -818,47 +1067,67 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
     a.g_scale = g_scale<DT>();
     const void* weight;
     int64_t ws;
-    launch_prep(a, c, sp, w, status, s, &weight, &ws);
-    for (int64_t v0 = 0; v0 < c.V; v0 += sp.piece) {
-        const int64_t words = std::min(sp.piece, c.V - v0);
-        const char* wp = static_cast<const char*>(weight) + 2 * v0 * ws;
-        Product p{};
-        p.count = a.count;
-        p.rows_cap = c.T;
-        p.status = status;
-        p.v0 = v0;
-        p.target = a.target;
-        p.lse = a.lse;
-        p.ratio = a.ratio;
-        p.g = w + sp.grad;
-        p.gld = sp.piece;
-        p.gmax = a.gmax;
-        p.inv_scale = 1.f / g_scale<DT>();
-        p.rows = a.rows;
-        p.tpad = sp.dpad;
-        Product q = p;
-        q.M = c.T; q.N = words; q.K = c.D;
-        cudaError_t e = launch_product<DT, USE_GRAD>(q, a.out, sp.dpad, wp, ws, s);
-        if (e == cudaSuccess && gh) {
-            q = p;
-            q.M = c.T; q.N = c.D; q.K = words;
-            q.first = v0 == 0;
-            q.last = v0 + words == c.V;
-            q.acc = q.first && q.last ? nullptr : reinterpret_cast<float*>(w + sp.acc);
-            q.out = gh; q.os = ghs;
-            q.vec = aligned16(gh) && ghs % 4 == 0;
-            e = launch_product<DT, USE_DH>(q, p.g, p.gld, wp, ws, s);
+    cudaError_t e = launch_prep(a, c, sp, w, status, s, &weight, &ws);
+    if (e != cudaSuccess) return e;
+    // step i: dH and dW of piece i - 1, G of piece i
+    for (int64_t i = 0; i <= sp.pieces; ++i) {
+        Batch batch{};
+        batch.count = a.count;
+        batch.next = a.next + i;
+        batch.status = status;
+        Product* dh = nullptr;
+        for (int64_t piece = i - 1; piece <= i; ++piece) {
+            if (piece < 0 || piece >= sp.pieces) continue;
+            const int64_t v0 = piece * sp.piece, words = std::min(sp.piece, c.V - v0);
+            const char* wp = static_cast<const char*>(weight) + 2 * v0 * ws;
+            Product p{};
+            p.rows_cap = c.T;
+            p.v0 = v0;
+            p.target = a.target;
+            p.lse = a.lse;
+            p.ratio = a.ratio;
+            p.g = w + sp.grad + (piece & 1) * sp.grad_bytes;
+            p.gld = sp.piece;
+            p.gmax = a.gmax;
+            p.inv_scale = 1.f / g_scale<DT>();
+            p.rows = a.rows;
+            p.acc = reinterpret_cast<float*>(w + sp.acc);
+            p.ald = sp.dpad;
+            if (piece == i) {
+                p.M = c.T; p.N = words; p.K = c.D;
+                if (!set_operands(p, DT, USE_GRAD, a.out, sp.dpad, wp, ws)) return cudaErrorInvalidValue;
+                batch.job[batch.njobs++] = p;
+                continue;
+            }
+            if (gh) {
+                Product q = p;
+                q.M = c.T; q.N = c.D; q.K = words;
+                q.first = piece == 0;
+                q.last = piece + 1 == sp.pieces;
+                q.out = gh; q.os = ghs;
+                q.vec = aligned16(gh) && ghs % 4 == 0;
+                if (!set_operands(q, DT, USE_DH, p.g, p.gld, wp, ws)) return cudaErrorInvalidValue;
+                dh = &batch.job[batch.njobs];
+                batch.job[batch.njobs++] = q;
+            }
+            if (gw) {
+                Product q = p;
+                q.M = words; q.N = c.D; q.K = c.T;
+                q.out = gw; q.os = gws; q.out_f32 = gw_f32; q.accumulate = accumulate;
+                q.vec = aligned16(gw) && gws % 4 == 0;
+                if (!set_operands(q, DT, USE_DW, p.g, p.gld, a.out, sp.dpad)) return cudaErrorInvalidValue;
+                batch.job[batch.njobs++] = q;
+            }
         }
-        if (e == cudaSuccess && gw) {
-            q = p;
-            q.M = words; q.N = c.D; q.K = c.T;
-            q.out = gw; q.os = gws; q.out_f32 = gw_f32; q.accumulate = accumulate;
-            q.vec = aligned16(gw) && gws % 4 == 0;
-            e = launch_product<DT, USE_DW>(q, p.g, p.gld, a.out, sp.dpad, s);
+        e = launch_products<DT>(batch, s);
+        if (e == cudaSuccess && dh && dh->last) {
+            const int64_t quads = c.T * (sp.dpad / 4);
+            e = launch_chained(finish_kernel<DT>, dim3(static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 4 * ddp::device_sm_count()))),
+                               256, 0, s, *dh, static_cast<const int32_t*>(a.count));
         }
         if (e != cudaSuccess) return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace
