@@ -264,10 +264,11 @@ copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, ui
 //   warp 10    (first CTA) claims tiles from a counter and passes them to both CTAs;
 //   warps 0-7  take finished tiles out of tensor memory, which holds two, so that
 //              a tile's epilogue runs under the next tile's products.
-// A launch runs up to three products, their tiles one after the other, longest
+// A launch runs one or several products, one a use at most, their tiles one after the other, longest
 // first: with dH and dW of one piece of the vocabulary comes G of the next, whose
 // short tiles fill what the long ones leave idle at the end.
-enum Use { USE_STATS, USE_GRAD, USE_DH, USE_DW };
+// what becomes of C, in the order in which a launch runs them
+enum Use { USE_DH, USE_DW, USE_GRAD, USE_STATS, kUses };
 
 constexpr int kTile = 256;               // rows and columns of a pair's tile
 constexpr int kHalf = 128;               // rows of A, of B and of C that one CTA holds
@@ -281,13 +282,12 @@ constexpr int kSlots = 4;                // claimed tiles on their way to the wa
 constexpr int kProductThreads = 32 * (kEpiWarps + 3);
 constexpr int kProductSmem = kStages * kStageBytes + kEpiWarps * kStagingBytes + 1024;
 constexpr int kGroup = 32;               // tiles along the fast side before the slow side moves on
-constexpr int kMaxJobs = 3;
 
+struct Maps {
+    CUtensorMap a, b;
+};
 struct Product {
-    CUtensorMap ta, tb;
-    int32_t use;
-    int32_t a_mn, b_mn;   // the operand's rows (not k) are contiguous in memory
-    int64_t M, N, K;
+    int64_t M, N, K;      // all zero: this use is not in the launch
     int64_t rows_cap;     // rows of the gathered arrays that exist
     int64_t v0;           // first word of the piece
     const int32_t* target;
@@ -311,9 +311,12 @@ struct Product {
     int64_t os;
     int32_t out_f32, accumulate, vec;
 };
+// The kernel's code is written out for each use, so that a product's arguments have
+// fixed places in the parameters: with an index that a tile brings along, a forward pass
+// at 4096 x 131072 x 4096 took 2.50 ms, with fixed places 2.22.
 struct Batch {
-    Product job[kMaxJobs];
-    int32_t njobs;
+    Maps map[kUses];
+    Product job[kUses];
     const int32_t* count; // gathered rows: bounds M (STATS, GRAD, DH) or K (DW)
     int32_t* next;        // tiles claimed beyond each pair's first
     int* status;
@@ -324,35 +327,35 @@ struct Shape {
     int32_t mt, nt, nkb, splits;
     int64_t M, tiles;
 };
-__device__ __forceinline__ Shape shape_of(const Product& p, int64_t count)
+__device__ __forceinline__ Shape shape_of(const Product& p, int use, int64_t count)
 {
     Shape s;
-    const int64_t K = p.use == USE_DW ? min(p.K, count) : p.K;
-    s.M = p.use == USE_DW ? p.M : min(p.M, count);
+    const int64_t K = use == USE_DW ? min(p.K, count) : p.K;
+    s.M = use == USE_DW ? p.M : min(p.M, count);
     s.mt = static_cast<int>((s.M + kTile - 1) / kTile);
     s.nt = static_cast<int>((p.N + kTile - 1) / kTile);
     s.nkb = static_cast<int>((K + kBlockK - 1) / kBlockK);
     // (the splits follow from the whole product's length, not this piece's: the sums' layout is the same for every piece)
-    s.splits = p.use == USE_DH && s.mt > 0 ? dh_splits(s.mt, s.nt, static_cast<int>((p.gld + kBlockK - 1) / kBlockK)) : 1;
+    s.splits = use == USE_DH && s.mt > 0 && s.nt > 0 ? dh_splits(s.mt, s.nt, static_cast<int>((p.gld + kBlockK - 1) / kBlockK)) : 1;
     s.tiles = static_cast<int64_t>(s.mt) * s.nt * s.splits;
     return s;
 }
 struct Tile {
-    int32_t job, m, n, split, kb0, kb1;  // job < 0: no more tiles
+    int32_t use, m, n, split, kb0, kb1;  // use < 0: no more tiles
     int32_t pad_[2];
 };
 // Tile t of a launch.  Tiles that run at the same time share operands: up to kGroup
 // along the side whose operand is the smaller one (the hidden states), then a
 // step along the other, so that the larger one is read from HBM once.
-__device__ __forceinline__ Tile tile_at(int64_t t, const Batch& b, const Shape* shapes)
+__device__ __forceinline__ Tile tile_at(int64_t t, const Shape* shapes)
 {
     Tile r{};
-    while (r.job + 1 < b.njobs && t >= shapes[r.job].tiles) t -= shapes[r.job++].tiles;
-    const Shape& s = shapes[r.job];
+    while (r.use + 1 < kUses && t >= shapes[r.use].tiles) t -= shapes[r.use++].tiles;
+    const Shape& s = shapes[r.use];
     const int64_t mn = static_cast<int64_t>(s.mt) * s.nt;
     r.split = static_cast<int>(t / mn);
     t -= r.split * mn;
-    const bool n_fast = b.job[r.job].use == USE_DW;
+    const bool n_fast = r.use == USE_DW;
     const int fast = n_fast ? s.nt : s.mt, slow = n_fast ? s.mt : s.nt;
     const int group = static_cast<int>(t / (static_cast<int64_t>(kGroup) * slow));
     const int64_t in = t - static_cast<int64_t>(group) * kGroup * slow;
@@ -366,10 +369,16 @@ __device__ __forceinline__ Tile tile_at(int64_t t, const Batch& b, const Shape* 
     return r;
 }
 
+// operands whose rows (not k) are contiguous in memory
+template <int USE> struct Majors {
+    static constexpr bool a_mn = USE == USE_DW;
+    static constexpr bool b_mn = USE == USE_DH || USE == USE_DW;
+};
+
 // one CTA's 128 rows of an operand, 64 of k: one box, or two where the rows are contiguous
-__device__ __forceinline__ void load_operand(bool mn, uint32_t dst, const CUtensorMap* map, int row, int k, uint32_t bar)
+template <bool MN> __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int k, uint32_t bar)
 {
-    if (mn) {
+    if (MN) {
         tensor_load(dst, map, row, k, bar);
         tensor_load(dst + kOperandBytes / 2, map, row + 64, k, bar);
     } else {
@@ -570,12 +579,35 @@ __device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, c
     }
 }
 
+// One thread copies a tile's operands, `it` stages into the ring.
+template <int USE>
+__device__ __forceinline__ bool copy_operands(const Batch& batch, int m, int n, const Tile& x, uint32_t it, uint32_t rank,
+                                              uint32_t base, uint32_t bar0, volatile int* dead)
+{
+    const uint32_t lead = cluster_addr(bar0, 0);
+    uint32_t s = it % kStages, parity = ((it / kStages) & 1) ^ 1;
+    for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        if (!bar_wait(bar0 + 8u * (kStages + s), parity, dead)) return false;
+        // both CTAs' bytes are counted on the first CTA's barrier
+        if (rank == 0) bar_expect(bar0 + 8u * s, 2 * kStageBytes);
+        const uint32_t a = base + s * kStageBytes;
+        load_operand<Majors<USE>::a_mn>(a, &batch.map[USE].a, m, kb * kBlockK, lead + 8u * s);
+        load_operand<Majors<USE>::b_mn>(a + kOperandBytes, &batch.map[USE].b, n, kb * kBlockK, lead + 8u * s);
+        if (++s == kStages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+    return true;
+}
+
 // One thread issues a tile's products, `it` stages into the ring.  It has the time of
 // four products (about 500 cycles) for each stage, so nothing but additions of
 // constants is left in the loop.
-template <int DT, bool A_MN, bool B_MN>
+template <int DT, int USE>
 __device__ __forceinline__ bool issue_products(uint32_t d, int blocks, uint32_t it, uint32_t base, uint32_t bar0, volatile int* dead)
 {
+    constexpr bool A_MN = Majors<USE>::a_mn, B_MN = Majors<USE>::b_mn;
     constexpr uint32_t desc = product_desc(DT == DDP_BF16, A_MN, B_MN, kTile, kTile);
     // rows contiguous: 8 k (1024 bytes) after 8 k, blocks of 64 rows apart; k contiguous: 16 k are 32 bytes
     constexpr uint64_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
@@ -602,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
 {
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kSlots];
-    __shared__ Shape shapes[kMaxJobs];
+    __shared__ Shape shapes[kUses];
     __shared__ uint32_t tmem_base;
     __shared__ __align__(16) Tile slot_tile[kSlots];
     __shared__ volatile int dead;
@@ -632,14 +664,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
             bar_init(sempty(i), 2 * kEpiWarps + 3);  // both CTAs' epilogue and copy warps, the product warp
         }
         bar_init_fence();
-        for (int i = 0; i < batch.njobs; ++i) {
-            tensor_map_prefetch(&batch.job[i].ta);
-            tensor_map_prefetch(&batch.job[i].tb);
+#pragma unroll
+        for (int i = 0; i < kUses; ++i) {
+            if (batch.job[i].M == 0) continue;
+            tensor_map_prefetch(&batch.map[i].a);
+            tensor_map_prefetch(&batch.map[i].b);
         }
     }
     if (warp == 9) tmem_alloc(smem_addr(&tmem_base), 512);
     wait_for_previous();
-    if (threadIdx.x < batch.njobs) shapes[threadIdx.x] = shape_of(batch.job[threadIdx.x], *batch.count);
+#pragma unroll
+    for (int i = 0; i < kUses; ++i)
+        if (threadIdx.x == 32 * i) shapes[i] = shape_of(batch.job[i], i, *batch.count);
     tmem_fence_before();
     __syncthreads();
     cluster_sync();
@@ -651,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
         const int s = i % kSlots;
         const bool ok = bar_wait(sfull(s), (i / kSlots) & 1, &dead);
         const uint4 lo = lds16(smem_addr(&slot_tile[s])), hi = lds16(smem_addr(&slot_tile[s]) + 16);
-        t->job = lo.x; t->m = lo.y; t->n = lo.z; t->split = lo.w;
+        t->use = lo.x; t->m = lo.y; t->n = lo.z; t->split = lo.w;
         t->kb0 = hi.x; t->kb1 = hi.y;
         return ok;
     };
@@ -662,22 +698,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
         // the products stand still for as long as their threads think
         if (rank == 0 && lane == 0) {
             int64_t total = 0;
-            for (int i = 0; i < batch.njobs; ++i) total += shapes[i].tiles;
+            for (int i = 0; i < kUses; ++i) total += shapes[i].tiles;
             const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
             for (uint32_t i = 0;; ++i) {
                 const int s = i % kSlots;
                 const int64_t t = i == 0 ? pair : npairs + static_cast<int64_t>(atomicAdd(batch.next, 1));
                 Tile x{};
-                if (t < total) x = tile_at(t, batch, shapes);
-                else x.job = -1;
+                if (t < total) x = tile_at(t, shapes);
+                else x.use = -1;
                 if (!bar_wait(sempty(s), ((i / kSlots) & 1) ^ 1, &dead)) break;
                 for (uint32_t r = 0; r < 2; ++r) {
                     const uint32_t at = cluster_addr(smem_addr(&slot_tile[s]), r);
-                    store_cluster(at, make_int4(x.job, x.m, x.n, x.split));
+                    store_cluster(at, make_int4(x.use, x.m, x.n, x.split));
                     store_cluster(at + 16, make_int4(x.kb0, x.kb1, 0, 0));
                     bar_arrive_cluster(cluster_addr(sfull(s), r));
                 }
-                if (x.job < 0) break;
+                if (x.use < 0) break;
             }
         }
     } else if (warp == 8) {
@@ -688,25 +724,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
                 Tile x;
                 if (!(ok = next_tile(i, &x))) break;
                 release_slot(i);
-                if (x.job < 0) break;
-                const Product& p = batch.job[x.job];
+                if (x.use < 0) break;
                 const int m = x.m * kTile + static_cast<int>(rank) * kHalf, n = x.n * kTile + static_cast<int>(rank) * kHalf;
-                const bool a_mn = p.a_mn, b_mn = p.b_mn;
-                const uint32_t lead = cluster_addr(bar0, 0);
-                uint32_t s = it % kStages, parity = ((it / kStages) & 1) ^ 1;
-                for (int kb = x.kb0; kb < x.kb1; ++kb, ++it) {
-                    if (!(ok = bar_wait(empty(s), parity, &dead))) break;
-                    // both CTAs' bytes are counted on the first CTA's barrier
-                    if (rank == 0) bar_expect(full(s), 2 * kStageBytes);
-                    const uint32_t bar = lead + 8u * s;
-                    const uint32_t a = base + s * kStageBytes;
-                    load_operand(a_mn, a, &p.ta, m, kb * kBlockK, bar);
-                    load_operand(b_mn, a + kOperandBytes, &p.tb, n, kb * kBlockK, bar);
-                    if (++s == kStages) {
-                        s = 0;
-                        parity ^= 1;
-                    }
-                }
+                if (x.use == USE_DH) ok = copy_operands<USE_DH>(batch, m, n, x, it, rank, base, bar0, &dead);
+                else if (x.use == USE_DW) ok = copy_operands<USE_DW>(batch, m, n, x, it, rank, base, bar0, &dead);
+                else if (x.use == USE_GRAD) ok = copy_operands<USE_GRAD>(batch, m, n, x, it, rank, base, bar0, &dead);
+                else ok = copy_operands<USE_STATS>(batch, m, n, x, it, rank, base, bar0, &dead);
+                it += x.kb1 - x.kb0;
             }
             // the last arrivals on this CTA's barriers come before it may leave
             for (int i = 0; ok && i < kStages; ++i, ++it) ok = bar_wait(empty(it % kStages), ((it / kStages) & 1) ^ 1, &dead);
@@ -719,17 +743,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
                 Tile x;
                 if (!(ok = next_tile(i, &x))) break;
                 release_slot(i);
-                if (x.job < 0) break;
+                if (x.use < 0) break;
                 if (x.kb0 == x.kb1) continue;
-                const Product& p = batch.job[x.job];
                 const int b = j & 1;
                 if (!(ok = bar_wait(tempty(b), ((j >> 1) & 1) ^ 1, &dead))) break;
                 tmem_fence_after();
                 const uint32_t d = tmem + b * kTile;
                 const int blocks = x.kb1 - x.kb0;
-                if (p.b_mn == 0) ok = issue_products<DT, false, false>(d, blocks, it, base, bar0, &dead);
-                else if (p.a_mn == 0) ok = issue_products<DT, false, true>(d, blocks, it, base, bar0, &dead);
-                else ok = issue_products<DT, true, true>(d, blocks, it, base, bar0, &dead);
+                if (x.use == USE_DH) ok = issue_products<DT, USE_DH>(d, blocks, it, base, bar0, &dead);
+                else if (x.use == USE_DW) ok = issue_products<DT, USE_DW>(d, blocks, it, base, bar0, &dead);
+                else ok = issue_products<DT, USE_GRAD>(d, blocks, it, base, bar0, &dead);  // and USE_STATS
                 it += blocks;
                 if (ok) product_commit(tfull(b));
                 ++j;
@@ -743,8 +766,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
             Tile x;
             if (!__all_sync(0xffffffffu, next_tile(i, &x))) break;
             if (lane == 0) release_slot(i);
-            if (x.job < 0) break;
-            const Product& p = batch.job[x.job];
+            if (x.use < 0) break;
             const bool none = x.kb0 == x.kb1;
             const int b = j & 1;
             if (!none) {
@@ -755,11 +777,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
             const int64_t m0 = static_cast<int64_t>(x.m) * kTile + rank * kHalf + quarter * 32;
             const int64_t n0 = static_cast<int64_t>(x.n) * kTile + half * kHalf;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * kTile + half * kHalf;
-            const Shape& sh = shapes[x.job];
-            if (p.use == USE_STATS) epilogue<DT, USE_STATS>(p, sh, x, taddr, none, m0, n0, staging, lane);
-            else if (p.use == USE_GRAD) epilogue<DT, USE_GRAD>(p, sh, x, taddr, none, m0, n0, staging, lane);
-            else if (p.use == USE_DH) epilogue<DT, USE_DH>(p, sh, x, taddr, none, m0, n0, staging, lane);
-            else epilogue<DT, USE_DW>(p, sh, x, taddr, none, m0, n0, staging, lane);
+            const Shape& sh = shapes[x.use];
+            if (x.use == USE_DH) epilogue<DT, USE_DH>(batch.job[USE_DH], sh, x, taddr, none, m0, n0, staging, lane);
+            else if (x.use == USE_DW) epilogue<DT, USE_DW>(batch.job[USE_DW], sh, x, taddr, none, m0, n0, staging, lane);
+            else if (x.use == USE_GRAD) epilogue<DT, USE_GRAD>(batch.job[USE_GRAD], sh, x, taddr, none, m0, n0, staging, lane);
+            else epilogue<DT, USE_STATS>(batch.job[USE_STATS], sh, x, taddr, none, m0, n0, staging, lane);
             tmem_fence_before();
             __syncwarp();
             if (lane == 0 && !none) bar_arrive_cluster(cluster_addr(tempty(b), 0));
@@ -787,7 +809,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Pro
 {
     using T = typename Elem<DT>::T;
     wait_for_previous();
-    const Shape sh = shape_of(p, *count);
+    const Shape sh = shape_of(p, USE_DH, *count);
     if (sh.splits == 1) return;
     const float alpha = *p.gmax * p.inv_scale;
     const int64_t quads = p.ald / 4, size = static_cast<int64_t>(sh.mt) * kTile * p.ald;
@@ -842,13 +864,13 @@ bool make_map(CUtensorMap* map, int dtype, const void* ptr, int64_t inner, int64
 }
 
 // the operands' maps: A is [M x K] and B [N x K] seen as stored, `*_stride` between stored rows
-bool set_operands(Product& p, int dtype, int use, const void* a, int64_t a_stride, const void* b, int64_t b_stride)
+template <int DT, int USE>
+bool set_product(Batch& batch, const Product& p, const void* a, int64_t a_stride, const void* b, int64_t b_stride)
 {
-    p.use = use;
-    p.a_mn = use == USE_DW;
-    p.b_mn = use == USE_DH || use == USE_DW;
-    return (p.a_mn ? make_map(&p.ta, dtype, a, p.M, p.K, a_stride, kBlockK) : make_map(&p.ta, dtype, a, p.K, p.M, a_stride, kHalf)) &&
-           (p.b_mn ? make_map(&p.tb, dtype, b, p.N, p.K, b_stride, kBlockK) : make_map(&p.tb, dtype, b, p.K, p.N, b_stride, kHalf));
+    batch.job[USE] = p;
+    Maps& m = batch.map[USE];
+    return (Majors<USE>::a_mn ? make_map(&m.a, DT, a, p.M, p.K, a_stride, kBlockK) : make_map(&m.a, DT, a, p.K, p.M, a_stride, kHalf)) &&
+           (Majors<USE>::b_mn ? make_map(&m.b, DT, b, p.N, p.K, b_stride, kBlockK) : make_map(&m.b, DT, b, p.K, p.N, b_stride, kHalf));
 }
 
 template <int DT> cudaError_t launch_products(const Batch& batch, cudaStream_t s)
@@ -876,11 +898,11 @@ template <int DT> cudaError_t launch_products(const Batch& batch, cudaStream_t s
         if (dev >= 0) cached[dev].store(pairs, std::memory_order_relaxed);
     }
     int64_t tiles = 0;
-    for (int i = 0; i < batch.njobs; ++i) {
+    for (int i = 0; i < kUses; ++i) {
         const Product& p = batch.job[i];
         const int64_t mt = (p.M + kTile - 1) / kTile, nt = (p.N + kTile - 1) / kTile;
         tiles += mt * nt;
-        if (p.use == USE_DH) tiles += kSplitTiles;  // fewer rows on the device may mean more splits
+        if (i == USE_DH && p.M) tiles += kSplitTiles;  // fewer rows on the device may mean more splits
     }
     cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
     // the cluster's size is the kernel's own; it may start while the kernel before it ends
@@ -1031,17 +1053,16 @@ template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* 
     cudaError_t e = launch_prep(a, c, sp, w, status, s, &weight, &ws);
     if (e != cudaSuccess) return e;
     Batch batch{};
-    batch.njobs = 1;
     batch.count = a.count;
     batch.next = a.next;
     batch.status = status;
-    Product& p = batch.job[0];
+    Product p{};
     p.M = c.T; p.N = c.V; p.K = c.D;
     p.target = a.target;
     p.part = reinterpret_cast<float2*>(w + sp.part);
     p.tpad = sp.tpad;
     p.ztarget = reinterpret_cast<float*>(w + sp.ztarget);
-    if (!set_operands(p, DT, USE_STATS, a.out, sp.dpad, weight, ws)) return cudaErrorInvalidValue;
+    if (!set_product<DT, USE_STATS>(batch, p, a.out, sp.dpad, weight, ws)) return cudaErrorInvalidValue;
     e = launch_products<DT>(batch, s);
     if (e != cudaSuccess) return e;
     return launch_chained(combine_kernel<DT>, dim3(static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows)), 32 * kJoinRows, 0, s,
@@ -1075,7 +1096,6 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
         batch.count = a.count;
         batch.next = a.next + i;
         batch.status = status;
-        Product* dh = nullptr;
         for (int64_t piece = i - 1; piece <= i; ++piece) {
             if (piece < 0 || piece >= sp.pieces) continue;
             const int64_t v0 = piece * sp.piece, words = std::min(sp.piece, c.V - v0);
@@ -1095,8 +1115,7 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
             p.ald = sp.dpad;
             if (piece == i) {
                 p.M = c.T; p.N = words; p.K = c.D;
-                if (!set_operands(p, DT, USE_GRAD, a.out, sp.dpad, wp, ws)) return cudaErrorInvalidValue;
-                batch.job[batch.njobs++] = p;
+                if (!set_product<DT, USE_GRAD>(batch, p, a.out, sp.dpad, wp, ws)) return cudaErrorInvalidValue;
                 continue;
             }
             if (gh) {
@@ -1106,24 +1125,21 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
                 q.last = piece + 1 == sp.pieces;
                 q.out = gh; q.os = ghs;
                 q.vec = aligned16(gh) && ghs % 4 == 0;
-                if (!set_operands(q, DT, USE_DH, p.g, p.gld, wp, ws)) return cudaErrorInvalidValue;
-                dh = &batch.job[batch.njobs];
-                batch.job[batch.njobs++] = q;
+                if (!set_product<DT, USE_DH>(batch, q, p.g, p.gld, wp, ws)) return cudaErrorInvalidValue;
             }
             if (gw) {
                 Product q = p;
                 q.M = words; q.N = c.D; q.K = c.T;
                 q.out = gw; q.os = gws; q.out_f32 = gw_f32; q.accumulate = accumulate;
                 q.vec = aligned16(gw) && gws % 4 == 0;
-                if (!set_operands(q, DT, USE_DW, p.g, p.gld, a.out, sp.dpad)) return cudaErrorInvalidValue;
-                batch.job[batch.njobs++] = q;
+                if (!set_product<DT, USE_DW>(batch, q, p.g, p.gld, a.out, sp.dpad)) return cudaErrorInvalidValue;
             }
         }
         e = launch_products<DT>(batch, s);
-        if (e == cudaSuccess && dh && dh->last) {
+        if (e == cudaSuccess && gh && i == sp.pieces) {
             const int64_t quads = c.T * (sp.dpad / 4);
             e = launch_chained(finish_kernel<DT>, dim3(static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 4 * ddp::device_sm_count()))),
-                               256, 0, s, *dh, static_cast<const int32_t*>(a.count));
+                               256, 0, s, batch.job[USE_DH], static_cast<const int32_t*>(a.count));
         }
         if (e != cudaSuccess) return e;
     }
