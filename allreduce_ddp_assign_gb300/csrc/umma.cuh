@@ -39,22 +39,31 @@ __device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
 }
-// `b` is an address in the cluster's shared memory
+// The same from afar, and a plain arrival (`b`: an address in the cluster's shared
+// memory).  Neither publishes memory to the cluster: what they announce is a count of
+// bytes, or that registers have been read.  (A release at cluster scope would wait for
+// all of the thread's stores to HBM.)
+__device__ __forceinline__ void bar_expect_cluster(uint32_t b, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t b)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
 }
-// 16 bytes of another CTA's shared memory (address in the cluster's shared memory)
-__device__ __forceinline__ void store_cluster(uint32_t a, int4 v)
+// 16 bytes into a CTA's shared memory, counted on that CTA's barrier (addresses in the cluster's shared memory)
+__device__ __forceinline__ void store_cluster(uint32_t a, int4 v, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity)
 {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(b), "r"(parity)

@@ -709,9 +709,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
                 if (!bar_wait(sempty(s), ((i / kSlots) & 1) ^ 1, &dead)) break;
                 for (uint32_t r = 0; r < 2; ++r) {
                     const uint32_t at = cluster_addr(smem_addr(&slot_tile[s]), r);
-                    store_cluster(at, make_int4(x.use, x.m, x.n, x.split));
-                    store_cluster(at + 16, make_int4(x.kb0, x.kb1, 0, 0));
-                    bar_arrive_cluster(cluster_addr(sfull(s), r));
+                    const uint32_t bar = cluster_addr(sfull(s), r);
+                    bar_expect_cluster(bar, sizeof(Tile));
+                    store_cluster(at, make_int4(x.use, x.m, x.n, x.split), bar);
+                    store_cluster(at + 16, make_int4(x.kb0, x.kb1, 0, 0), bar);
                 }
                 if (x.use < 0) break;
             }
