@@ -516,62 +516,76 @@ __device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, c
         const bool sums = USE == USE_DH && !(p.first && p.last && shape.splits == 1);
         const bool result = USE != USE_DH || (p.last && shape.splits == 1);
         float* acc = p.acc + static_cast<int64_t>(tile.split) * shape.mt * kTile * p.ald;
+        const bool adds = sums ? !p.first : USE == USE_DW && p.accumulate;
+        const bool f32 = USE == USE_DW && p.out_f32;
+        const int32_t token = USE == USE_DH && result && m < M ? p.rows[m] : 0;
         for (int q = 0; q < 4; ++q) {
-            tile_values(taddr + q * 32, empty, c);
+            const int64_t n = n0 + q * 32 + (lane & 7) * 4;
             if (n0 + q * 32 >= p.N) break;
+            const int width = static_cast<int>(max(int64_t{0}, min(int64_t{4}, p.N - n)));
+            const bool wide = p.vec && width == 4;
+            // what is added to, all of it on its way before the first value is needed
+            float old[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t row = m0 + i * 4 + (lane >> 3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) old[i][j] = 0.f;
+                if (!adds || row >= M || width == 0) continue;
+                if (sums) {
+                    *reinterpret_cast<float4*>(old[i]) = *reinterpret_cast<const float4*>(acc + row * p.ald + n);  // ald: a multiple of 8
+                } else if (f32) {
+                    const float* o = static_cast<const float*>(p.out) + (p.v0 + row) * p.os + n;
+                    if (wide) *reinterpret_cast<float4*>(old[i]) = *reinterpret_cast<const float4*>(o);
+                    else
+                        for (int j = 0; j < 4; ++j) old[i][j] = j < width ? o[j] : 0.f;
+                } else {
+                    const T* o = static_cast<const T*>(p.out) + (p.v0 + row) * p.os + n;
+                    if (wide) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(o);
+                        const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) old[i][j] = Elem<DT>::to_f(t[j]);
+                    } else {
+                        for (int j = 0; j < 4; ++j) old[i][j] = j < width ? Elem<DT>::to_f(o[j]) : 0.f;
+                    }
+                }
+            }
+            tile_values(taddr + q * 32, empty, c);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 sts16(staged(staging, lane, k), make_uint4(__float_as_uint(c[4 * k]), __float_as_uint(c[4 * k + 1]),
                                                            __float_as_uint(c[4 * k + 2]), __float_as_uint(c[4 * k + 3])));
             __syncwarp();
-            const int64_t n = n0 + q * 32 + (lane & 7) * 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = i * 4 + (lane >> 3);
+                const int32_t to = USE == USE_DH ? __shfl_sync(0xffffffffu, token, r) : 0;
                 const uint4 raw = lds16(staged(staging, r, lane & 7));
                 float x[4] = {__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w)};
                 const int64_t row = m0 + r;
-                if (row >= M || n >= p.N) continue;
-                const int width = static_cast<int>(min(static_cast<int64_t>(4), p.N - n));
+                if (row >= M || width == 0) continue;
                 if (sums) {
-                    float* a = acc + row * p.ald + n;  // ald is a multiple of 8
-                    if (!p.first) {
-                        const float4 o = *reinterpret_cast<const float4*>(a);
-                        x[0] += o.x; x[1] += o.y; x[2] += o.z; x[3] += o.w;
-                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] += old[i][j];
                     if (!result) {
-                        *reinterpret_cast<float4*>(a) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4*>(acc + row * p.ald + n) = make_float4(x[0], x[1], x[2], x[3]);
                         continue;
                     }
                 }
-                const int64_t at = (USE == USE_DH ? p.rows[row] : p.v0 + row) * p.os + n;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= alpha;
-                if (USE == USE_DW && p.out_f32) {
+                for (int j = 0; j < 4; ++j) x[j] = x[j] * alpha + (USE == USE_DW ? old[i][j] : 0.f);
+                const int64_t at = (USE == USE_DH ? to : p.v0 + row) * p.os + n;
+                if (f32) {
                     float* o = static_cast<float*>(p.out) + at;
-                    if (p.vec && width == 4) {
-                        if (p.accumulate) {
-                            const float4 v = *reinterpret_cast<const float4*>(o);
-                            x[0] += v.x; x[1] += v.y; x[2] += v.z; x[3] += v.w;
-                        }
-                        *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
-                    } else {
-                        for (int j = 0; j < width; ++j) o[j] = x[j] + (p.accumulate ? o[j] : 0.f);
-                    }
+                    if (wide) *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+                    else
+                        for (int j = 0; j < width; ++j) o[j] = x[j];
                 } else {
                     T* o = static_cast<T*>(p.out) + at;
-                    if (p.vec && width == 4) {
-                        if (USE == USE_DW && p.accumulate) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(o);
-                            const T* t = reinterpret_cast<const T*>(&v);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) x[j] += Elem<DT>::to_f(t[j]);
-                        }
-                        *reinterpret_cast<uint2*>(o) = make_uint2(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]));
-                    } else {
-                        for (int j = 0; j < width; ++j)
-                            o[j] = Elem<DT>::from_f(x[j] + (USE == USE_DW && p.accumulate ? Elem<DT>::to_f(o[j]) : 0.f));
-                    }
+                    if (wide) *reinterpret_cast<uint2*>(o) = make_uint2(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]));
+                    else
+                        for (int j = 0; j < width; ++j) o[j] = Elem<DT>::from_f(x[j]);
                 }
             }
             __syncwarp();
