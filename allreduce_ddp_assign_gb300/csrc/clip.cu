@@ -3,11 +3,13 @@
 //   n = sqrt(sum_k sum_i g_k[i]^2)  or  max |g_k[i]|,   c = min(1, max_norm / (n + 1e-6)),   g_k[i] <- c g_k[i]
 //
 // The tensors are laid end to end in one element space (their lengths' prefix
-// sums); each CTA takes an equal contiguous slice and walks the tensors in it,
-// so hundreds of small tensors cost no more launches than one large one.
+// sums).  A CTA takes a contiguous slice of it, its warps take turns of kTurn elements,
+// and each walks the tensors in its turn by itself, so that hundreds of small tensors
+// cost neither more launches nor a wait for each.
 //
-// HBM-bound: one pass reads every element for the norm, a second reads and
-// writes it.  The factor is known only when the last element has been read.
+// HBM-bound: one pass reads every element for the norm, a second reads and writes
+// it; the factor is known only when the last element has been read.  The second
+// pass goes backwards, where the first one's last elements are still in L2.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -17,8 +19,18 @@
 namespace ddplm {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPerSm = 3;        // CTAs of the two passes on an SM
+constexpr int kTurn = 2048;      // elements of a warp's turn: 16 (fp32) or 8 vectors a lane
+constexpr int kBatch = 4;        // vectors a lane keeps in flight (two in the cluster, whose threads have fewer registers)
+constexpr int kWindow = kThreads;  // tensors whose tables a CTA holds at a time
 constexpr int kMaxGrid = DDP_CLIP_WORKSPACE_BYTES / 8;  // one double of partial result a CTA
+// Up to here one cluster of 16 CTAs does both passes: the norm crosses its shared memory
+// instead of a second launch.
+constexpr int64_t kClusterElements = 400000;
+constexpr int kClusterCtas = 16;
+constexpr int kClusterThreads = 1024;
 
 struct ClipArgs {
     const void* const* grads;
@@ -30,57 +42,88 @@ struct ClipArgs {
     double* part;
     float* norm;
     float max_norm;
+    int32_t clip;
 };
 
-// the last tensor that starts at or before element e (empty tensors before it are skipped over)
-__device__ __forceinline__ int find_tensor(const int64_t* offset, int n, int64_t e)
+// A CTA's view of the tables: `count` tensors from `first`.
+template <int N> struct Window {
+    int64_t offset[N + 1];
+    const void* grad[N];
+    void* out[N];
+    int32_t dtype[N];
+    int32_t first, count;
+};
+
+// Loads the tables from tensor `first` on; every thread calls it.
+template <int N> __device__ __forceinline__ void load_window(Window<N>& w, const ClipArgs& a, int first)
 {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (offset[mid] <= e) lo = mid;
-        else hi = mid - 1;
+    __syncthreads();
+    const int i = threadIdx.x;
+    const int count = min(N, a.ntensors - first);
+    if (i < count) {
+        w.offset[i] = a.offset[first + i];
+        w.grad[i] = a.grads[first + i];
+        w.out[i] = a.out ? a.out[first + i] : const_cast<void*>(w.grad[i]);
+        w.dtype[i] = a.dtypes[first + i];
+        if (i == count - 1) w.offset[count] = a.offset[first + count];
     }
-    return lo;
+    if (i == 0) {
+        w.first = first;
+        w.count = count;
+    }
+    __syncthreads();
+}
+
+// The last tensor that starts at or before element e, found by all threads together.
+__device__ __forceinline__ int find_tensor(const ClipArgs& a, int64_t e)
+{
+    int k = -1;
+    for (int base = 0; base < a.ntensors; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        k += __syncthreads_count(i < a.ntensors && a.offset[i] <= e);
+    }
+    return k;
 }
 
 // A value's square is exact enough in fp32 while it stays well inside its range:
-// a vector whose largest magnitude lies outside [2^-40, 2^60] is squared in fp64.
+// values whose largest magnitude lies outside [2^-40, 2^60] are squared in fp64.
 __device__ __forceinline__ bool fp32_square_range(float m) { return m >= 0x1p-40f && m <= 0x1p60f; }
 
-template <int DT, bool INF> struct Accum {
-    // sum of squares (fp64) or largest magnitude of N values
-    template <int N> __device__ __forceinline__ static void add(double& acc, const float (&x)[N])
-    {
-        if (INF) {
-            float m = static_cast<float>(acc);
-#pragma unroll
-            for (int j = 0; j < N; ++j) m = (fabsf(x[j]) > m || x[j] != x[j]) ? fabsf(x[j]) : m;  // a NaN stays
-            acc = m;
-        } else {
-            float m = 0.f, s = 0.f;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                m = fmaxf(m, fabsf(x[j]));
-                s = fmaf(x[j], x[j], s);
-            }
-            if (fp32_square_range(m)) {
-                acc += static_cast<double>(s);
-            } else if (!(s == 0.f && m == 0.f)) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) acc += static_cast<double>(x[j]) * static_cast<double>(x[j]);
-            }
-        }
-    }
-};
-
-// largest magnitude where a NaN beats everything
+// larger magnitude where a NaN beats everything
 __device__ __forceinline__ double pick_max(double a, double b) { return (b > a || b != b) ? b : a; }
-
 template <bool INF> __device__ __forceinline__ double join(double a, double b)
 {
     if (INF) return a != a ? a : pick_max(a, b);
     return a + b;
+}
+
+// N values (at most 32) into the sum of squares, in fp32 and then once in fp64, or into the largest magnitude.
+template <bool INF, int N> __device__ __forceinline__ void add_values(double& acc, const float (&x)[N])
+{
+    float m = 0.f;
+    if (INF) {
+        float bad = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            m = fmaxf(m, fabsf(x[j]));
+            bad = x[j] != x[j] ? x[j] : bad;
+        }
+        acc = join<true>(acc, bad != bad ? bad : m);
+        return;
+    }
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        m = fmaxf(m, fabsf(x[j]));
+        if (j & 1) s1 = fmaf(x[j], x[j], s1);
+        else s0 = fmaf(x[j], x[j], s0);
+    }
+    if (fp32_square_range(m)) {
+        acc += static_cast<double>(s0 + s1);
+    } else if (!(s0 + s1 == 0.f && m == 0.f)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc = fma(static_cast<double>(x[j]), static_cast<double>(x[j]), acc);
+    }
 }
 
 // Every thread gets the CTA's joined value; the order is fixed.
@@ -97,57 +140,164 @@ template <bool INF> __device__ double block_join(double v)
     return r;
 }
 
-template <int DT, bool INF>
-__device__ __forceinline__ void norm_piece(const void* base, int64_t i0, int64_t n, double& acc)
+// elements before the first 16-byte boundary, at most n
+template <typename T> __device__ __forceinline__ int head_of(const T* p, int n)
+{
+    return min(n, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T)));
+}
+
+// one warp, n <= kTurn values of one tensor
+template <int DT, bool INF, int B> __device__ __forceinline__ void norm_piece(const void* base, int64_t i0, int n, int lane, double& acc)
 {
     using T = typename Elem<DT>::T;
     constexpr int N = Vec<DT>::N;
     const T* p = static_cast<const T*>(base) + i0;
-    int64_t head = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
-    if (head > n) head = n;
-    const int64_t nv = (n - head) / N;
-    const int64_t tail = head + nv * N;
-    for (int64_t i = threadIdx.x; i < head; i += blockDim.x) {
-        const float x[1] = {Elem<DT>::to_f(p[i])};
-        Accum<DT, INF>::template add<1>(acc, x);
-    }
+    const int head = head_of(p, n), nv = (n - head) / N, tail = head + nv * N;
+    // the ragged ends: fewer than 32 values each
+    float e[2] = {lane < head ? Elem<DT>::to_f(p[lane]) : 0.f, tail + lane < n ? Elem<DT>::to_f(p[tail + lane]) : 0.f};
     const Vec<DT>* pv = reinterpret_cast<const Vec<DT>*>(p + head);
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
+    int i = lane;
+    for (; i + 32 * (B - 1) < nv; i += 32 * B) {
+        Vec<DT> v[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) v[u] = pv[i + 32 * u];
+        float x[B * N];
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[u * N + j] = Elem<DT>::to_f(v[u].v[j]);
+        add_values<INF>(acc, x);
+    }
+    for (; i < nv; i += 32) {
         const Vec<DT> v = pv[i];
         float x[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] = Elem<DT>::to_f(v.v[j]);
-        Accum<DT, INF>::template add<N>(acc, x);
+        add_values<INF>(acc, x);
     }
-    for (int64_t i = tail + threadIdx.x; i < n; i += blockDim.x) {
-        const float x[1] = {Elem<DT>::to_f(p[i])};
-        Accum<DT, INF>::template add<1>(acc, x);
+    add_values<INF>(acc, e);
+}
+
+template <int DT, int B> __device__ __forceinline__ void scale_piece(const void* src, void* dst, int64_t i0, int n, int lane, float c)
+{
+    using T = typename Elem<DT>::T;
+    constexpr int N = Vec<DT>::N;
+    const T* p = static_cast<const T*>(src) + i0;
+    T* q = static_cast<T*>(dst) + i0;
+    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) {
+        // vectors need both sides at the same place within 16 bytes
+        for (int i = lane; i < n; i += 32 * B) {
+            T v[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                if (i + 32 * u < n) v[u] = p[i + 32 * u];
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                if (i + 32 * u < n) q[i + 32 * u] = Elem<DT>::from_f(Elem<DT>::to_f(v[u]) * c);
+        }
+        return;
+    }
+    const int head = head_of(p, n), nv = (n - head) / N, tail = head + nv * N;
+    if (lane < head) q[lane] = Elem<DT>::from_f(Elem<DT>::to_f(p[lane]) * c);
+    if (tail + lane < n) q[tail + lane] = Elem<DT>::from_f(Elem<DT>::to_f(p[tail + lane]) * c);
+    const Vec<DT>* pv = reinterpret_cast<const Vec<DT>*>(p + head);
+    Vec<DT>* qv = reinterpret_cast<Vec<DT>*>(q + head);
+    for (int i = lane; i < nv; i += 32 * B) {
+        Vec<DT> v[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            if (i + 32 * u < nv) v[u] = pv[i + 32 * u];
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            if (i + 32 * u >= nv) continue;
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[u].v[j] = Elem<DT>::from_f(Elem<DT>::to_f(v[u].v[j]) * c);
+            // the results are not read again here: they leave L2 first
+            __stcs(reinterpret_cast<uint4*>(qv + i + 32 * u), *reinterpret_cast<const uint4*>(&v[u]));
+        }
     }
 }
 
-template <bool INF> __global__ void __launch_bounds__(kThreads) norm_kernel(ClipArgs a)
-{
-    const int64_t e0 = a.total / gridDim.x * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), a.total % gridDim.x);
-    const int64_t e1 = e0 + a.total / gridDim.x + (blockIdx.x < a.total % gridDim.x);
+// What a walk over the elements does with a piece of a tensor.
+template <bool INF, int B> struct NormWalk {
     double acc = 0.0;
-    if (e0 < e1) {
-        int k = find_tensor(a.offset, a.ntensors, e0);
-        for (int64_t e = e0; e < e1 && k < a.ntensors; ++k) {
-            const int64_t lo = a.offset[k], hi = a.offset[k + 1];
-            const int64_t end = hi < e1 ? hi : e1;
-            if (end <= e) continue;
-            const void* g = a.grads[k];
-            if (g) {
-                const int dt = a.dtypes[k];
-                if (dt == DDP_F32) norm_piece<DDP_F32, INF>(g, e - lo, end - e, acc);
-                else if (dt == DDP_BF16) norm_piece<DDP_BF16, INF>(g, e - lo, end - e, acc);
-                else norm_piece<DDP_F16, INF>(g, e - lo, end - e, acc);
-            }
-            e = end;
-        }
+    template <int N> __device__ __forceinline__ void piece(const Window<N>& w, int k, int64_t i0, int n, int lane)
+    {
+        if (!w.grad[k]) return;
+        if (w.dtype[k] == DDP_F32) norm_piece<DDP_F32, INF, B>(w.grad[k], i0, n, lane, acc);
+        else if (w.dtype[k] == DDP_BF16) norm_piece<DDP_BF16, INF, B>(w.grad[k], i0, n, lane, acc);
+        else norm_piece<DDP_F16, INF, B>(w.grad[k], i0, n, lane, acc);
     }
-    const double r = block_join<INF>(acc);
+};
+template <int B> struct ScaleWalk {
+    float c;
+    template <int N> __device__ __forceinline__ void piece(const Window<N>& w, int k, int64_t i0, int n, int lane)
+    {
+        if (!w.grad[k] || !w.out[k]) return;
+        if (w.dtype[k] == DDP_F32) scale_piece<DDP_F32, B>(w.grad[k], w.out[k], i0, n, lane, c);
+        else if (w.dtype[k] == DDP_BF16) scale_piece<DDP_BF16, B>(w.grad[k], w.out[k], i0, n, lane, c);
+        else scale_piece<DDP_F16, B>(w.grad[k], w.out[k], i0, n, lane, c);
+    }
+};
+
+// One CTA's walk over [e0, e1), in strides of `warps` turns of `turn` elements, from the
+// end where BACK.  The window holds the tensors of the slice; where it does not hold all
+// of them the slice is walked in parts, a window each.
+template <bool BACK, typename F, int N>
+__device__ __forceinline__ void walk(Window<N>& w, const ClipArgs& a, int first, int64_t e0, int64_t e1, int turn, F& f)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (w.first != first) load_window(w, a, first);
+    for (int64_t s0 = e0; s0 < e1;) {
+        const int64_t s1 = min(e1, w.offset[w.count]);
+        const int64_t turns = (s1 - s0 + turn - 1) / turn;
+        int k = BACK ? w.count - 1 : 0;
+        for (int64_t j = warp; j < turns; j += warps) {
+            const int64_t t0 = s0 + (BACK ? turns - 1 - j : j) * turn, t1 = min(s1, t0 + turn);
+            // the tensor of the turn's first element (k only ever moves one way)
+            if (BACK)
+                while (w.offset[k] > t0) --k;
+            else
+                while (w.offset[k + 1] <= t0) ++k;
+            int kk = k;
+            for (int64_t e = t0; e < t1; ++kk) {
+                const int64_t end = min(t1, w.offset[kk + 1]);
+                if (end <= e) continue;
+                f.piece(w, kk, e - w.offset[kk], static_cast<int>(end - e), lane);
+                e = end;
+            }
+        }
+        s0 = s1;
+        if (s0 >= e1 || w.first + w.count >= a.ntensors) break;
+        load_window(w, a, w.first + w.count);
+    }
+}
+
+__device__ __forceinline__ void slice_of(const ClipArgs& a, int cta, int ctas, int64_t* e0, int64_t* e1)
+{
+    const int64_t per = a.total / ctas, more = a.total % ctas;
+    *e0 = per * cta + min(static_cast<int64_t>(cta), more);
+    *e1 = *e0 + per + (cta < more);
+}
+
+__device__ __forceinline__ float factor(const ClipArgs& a, float norm)
+{
+    const float ratio = a.max_norm / (norm + 1e-6f);
+    return ratio > 1.f ? 1.f : ratio;  // a NaN stays
+}
+
+template <bool INF> __global__ void __launch_bounds__(kThreads, kPerSm) norm_kernel(const __grid_constant__ ClipArgs a)
+{
+    __shared__ Window<kWindow> w;
+    wait_for_previous();
+    allow_next();
+    int64_t e0, e1;
+    slice_of(a, blockIdx.x, gridDim.x, &e0, &e1);
+    NormWalk<INF, kBatch> f;
+    if (threadIdx.x == 0) w.first = -1;
+    __syncthreads();
+    if (e0 < e1) walk<false>(w, a, a.ntensors <= kWindow ? 0 : find_tensor(a, e0), e0, e1, kTurn, f);
+    const double r = block_join<INF>(f.acc);
     if (threadIdx.x == 0) a.part[blockIdx.x] = r;
 }
 
@@ -162,67 +312,69 @@ template <bool INF> __device__ float total_norm(const double* part, int n)
 
 template <bool INF> __global__ void __launch_bounds__(kThreads) norm_end_kernel(const double* part, int n, float* norm)
 {
+    wait_for_previous();
     const float r = total_norm<INF>(part, n);
     if (threadIdx.x == 0) *norm = r;
 }
 
-template <int DT>
-__device__ __forceinline__ void scale_piece(const void* src, void* dst, int64_t i0, int64_t n, float c)
+template <bool INF> __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_constant__ ClipArgs a)
 {
-    using T = typename Elem<DT>::T;
-    constexpr int N = Vec<DT>::N;
-    const T* p = static_cast<const T*>(src) + i0;
-    T* q = static_cast<T*>(dst) + i0;
-    int64_t head = ((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T);
-    // vectors where both sides share their place within 16 bytes
-    if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) || head > n) head = n;
-    const int64_t nv = (n - head) / N;
-    const int64_t tail = head + nv * N;
-    for (int64_t i = threadIdx.x; i < head; i += blockDim.x) q[i] = Elem<DT>::from_f(Elem<DT>::to_f(p[i]) * c);
-    const Vec<DT>* pv = reinterpret_cast<const Vec<DT>*>(p + head);
-    Vec<DT>* qv = reinterpret_cast<Vec<DT>*>(q + head);
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
-        Vec<DT> v = pv[i];
-#pragma unroll
-        for (int j = 0; j < N; ++j) v.v[j] = Elem<DT>::from_f(Elem<DT>::to_f(v.v[j]) * c);
-        qv[i] = v;
-    }
-    for (int64_t i = tail + threadIdx.x; i < n; i += blockDim.x) q[i] = Elem<DT>::from_f(Elem<DT>::to_f(p[i]) * c);
-}
-
-template <bool INF> __global__ void __launch_bounds__(kThreads) scale_kernel(ClipArgs a, int nparts)
-{
-    const float norm = total_norm<INF>(a.part, nparts);
+    __shared__ Window<kWindow> w;
+    int64_t e0, e1;
+    slice_of(a, blockIdx.x, gridDim.x, &e0, &e1);
+    // The tables are older than the norm pass, which let this kernel start: they are read
+    // before that pass has ended.
+    const int first = e0 < e1 && a.ntensors > kWindow ? find_tensor(a, e0) : 0;
+    if (e0 < e1) load_window(w, a, first);
+    wait_for_previous();
+    const float norm = total_norm<INF>(a.part, gridDim.x);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-    const float ratio = a.max_norm / (norm + 1e-6f);
-    const float c = ratio > 1.f ? 1.f : ratio;  // a NaN stays
-    if (c == 1.f && !a.out) return;
-    const int64_t e0 = a.total / gridDim.x * blockIdx.x + min(static_cast<int64_t>(blockIdx.x), a.total % gridDim.x);
-    const int64_t e1 = e0 + a.total / gridDim.x + (blockIdx.x < a.total % gridDim.x);
-    if (e0 >= e1) return;
-    int k = find_tensor(a.offset, a.ntensors, e0);
-    for (int64_t e = e0; e < e1 && k < a.ntensors; ++k) {
-        const int64_t lo = a.offset[k], hi = a.offset[k + 1];
-        const int64_t end = hi < e1 ? hi : e1;
-        if (end <= e) continue;
-        const void* g = a.grads[k];
-        void* o = a.out ? a.out[k] : const_cast<void*>(g);
-        if (g && o) {
-            const int dt = a.dtypes[k];
-            if (dt == DDP_F32) scale_piece<DDP_F32>(g, o, e - lo, end - e, c);
-            else if (dt == DDP_BF16) scale_piece<DDP_BF16>(g, o, e - lo, end - e, c);
-            else scale_piece<DDP_F16>(g, o, e - lo, end - e, c);
-        }
-        e = end;
-    }
+    const float c = factor(a, norm);
+    if (e0 >= e1 || (c == 1.f && !a.out)) return;
+    ScaleWalk<kBatch> f{c};
+    walk<true>(w, a, first, e0, e1, kTurn, f);
 }
 
-// one wave of CTAs at most, 4096 elements a CTA at least
+// Both passes by one cluster: the CTAs' partial results cross its shared memory, and the
+// second pass finds the elements in L1 or L2.
+template <bool INF> __global__ void __launch_bounds__(kClusterThreads) cluster_kernel(const __grid_constant__ ClipArgs a)
+{
+    __shared__ Window<kWindow> w;
+    __shared__ double parts[kClusterCtas];
+    int64_t e0, e1;
+    slice_of(a, blockIdx.x, gridDim.x, &e0, &e1);
+    const int turn = static_cast<int>(((e1 - e0) / (kClusterThreads / 32) + 256) / 256 * 256);
+    if (threadIdx.x == 0) w.first = -1;
+    __syncthreads();
+    wait_for_previous();
+    const int first = e0 < e1 && a.ntensors > kWindow ? find_tensor(a, e0) : 0;
+    NormWalk<INF, 2> f;
+    if (e0 < e1) walk<false>(w, a, first, e0, e1, turn, f);
+    const double r = block_join<INF>(f.acc);
+    if (threadIdx.x < gridDim.x) {
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(at)
+            : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&parts[blockIdx.x]))), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(r) : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    double acc = 0.0;
+    for (int i = 0; i < static_cast<int>(gridDim.x); ++i) acc = join<INF>(acc, parts[i]);
+    const float norm = INF ? static_cast<float>(acc) : static_cast<float>(sqrt(acc));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+    if (!a.clip) return;
+    const float c = factor(a, norm);
+    if (e0 >= e1 || (c == 1.f && !a.out)) return;
+    ScaleWalk<2> s{c};
+    walk<false>(w, a, first, e0, e1, turn, s);
+}
+
+// one wave of CTAs at most, a turn for each warp at least
 int grid_for(int64_t total)
 {
-    const int64_t want = (total + 4095) / 4096;
-    const int64_t wave = static_cast<int64_t>(ddp::device_sm_count()) * 4;
+    const int64_t want = (total + kTurn * kWarps - 1) / (kTurn * kWarps);
+    const int64_t wave = static_cast<int64_t>(ddp::device_sm_count()) * kPerSm;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, wave, kMaxGrid})));
 }
 
@@ -244,20 +396,55 @@ ddp_status check(const char* fn, const ClipArgs& a, int32_t norm_type, const voi
     return DDP_OK;
 }
 
-ddp_status launch(const char* fn, const ClipArgs& a, bool inf, bool clip, void* stream)
+template <bool INF> cudaError_t launch_cluster(const ClipArgs& a, cudaStream_t s)
+{
+    // 16 CTAs are more than every device promises to run as a cluster: asked for once a device
+    static std::atomic<int> cached[ddp::kMaxDevices] = {};
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    const int dev = ddp::current_device();
+    int ctas = dev >= 0 ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (!ctas) {
+        cudaError_t e = cudaFuncSetAttribute(cluster_kernel<INF>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        cfg.numAttrs = 1;
+        for (ctas = kClusterCtas; ctas > 1; ctas /= 2) {
+            cfg.gridDim = dim3(ctas);
+            at[0].val.clusterDim.x = ctas;
+            if (cudaOccupancyMaxActiveClusters(&n, cluster_kernel<INF>, &cfg) == cudaSuccess && n > 0) break;
+        }
+        (void)cudaGetLastError();
+        if (dev >= 0) cached[dev].store(ctas, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3(ctas);
+    at[0].val.clusterDim.x = ctas;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, cluster_kernel<INF>, a);
+}
+
+template <bool INF> cudaError_t launch_as(const ClipArgs& a, cudaStream_t s)
+{
+    if (a.total <= kClusterElements) return launch_cluster<INF>(a, s);
+    const dim3 grid(grid_for(a.total));
+    const cudaError_t e = launch_chained(norm_kernel<INF>, grid, kThreads, 0, s, a);
+    if (e != cudaSuccess) return e;
+    if (a.clip) return launch_chained(scale_kernel<INF>, grid, kThreads, 0, s, a);
+    return launch_chained(norm_end_kernel<INF>, dim3(1), kThreads, 0, s, static_cast<const double*>(a.part),
+                          static_cast<int>(grid.x), a.norm);
+}
+
+ddp_status launch(const char* fn, const ClipArgs& a, bool inf, void* stream)
 {
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int grid = grid_for(a.total);
-    if (inf) norm_kernel<true><<<grid, kThreads, 0, s>>>(a);
-    else norm_kernel<false><<<grid, kThreads, 0, s>>>(a);
-    if (clip) {
-        if (inf) scale_kernel<true><<<grid, kThreads, 0, s>>>(a, grid);
-        else scale_kernel<false><<<grid, kThreads, 0, s>>>(a, grid);
-    } else {
-        if (inf) norm_end_kernel<true><<<1, kThreads, 0, s>>>(a.part, grid, a.norm);
-        else norm_end_kernel<false><<<1, kThreads, 0, s>>>(a.part, grid, a.norm);
-    }
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = inf ? launch_as<true>(a, s) : launch_as<false>(a, s);
     if (err != cudaSuccess) return ddp::fail(DDP_E_CUDA, "%s: kernel launch failed: %s", fn, cudaGetErrorString(err));
     return ddp::ok();
 }
@@ -269,10 +456,10 @@ extern "C" ddp_status ddp_grad_norm(const void* const* grads, const int64_t* off
                                     int32_t ntensors, int64_t total, int32_t norm_type, float* norm, void* workspace,
                                     int64_t workspace_bytes, void* stream)
 {
-    const ddplm::ClipArgs a{grads, nullptr, offset, dtypes, ntensors, total, static_cast<double*>(workspace), norm, 0.f};
+    const ddplm::ClipArgs a{grads, nullptr, offset, dtypes, ntensors, total, static_cast<double*>(workspace), norm, 0.f, 0};
     const ddp_status st = ddplm::check("ddp_grad_norm", a, norm_type, workspace, workspace_bytes);
     if (st != DDP_OK) return st;
-    return ddplm::launch("ddp_grad_norm", a, norm_type == DDP_NORM_INF, false, stream);
+    return ddplm::launch("ddp_grad_norm", a, norm_type == DDP_NORM_INF, stream);
 }
 
 extern "C" ddp_status ddp_clip_grads(const void* const* grads, void* const* out, const int64_t* offset,
@@ -282,9 +469,9 @@ extern "C" ddp_status ddp_clip_grads(const void* const* grads, void* const* out,
 {
     const char* fn = "ddp_clip_grads";
     const ddplm::ClipArgs a{grads, out, offset, dtypes, ntensors, total, static_cast<double*>(workspace), norm,
-                            max_norm};
+                            max_norm, 1};
     const ddp_status st = ddplm::check(fn, a, norm_type, workspace, workspace_bytes);
     if (st != DDP_OK) return st;
     if (!(max_norm >= 0.f)) return ddp::fail(DDP_E_INVAL, "%s: max_norm = %g is negative or NaN", fn, max_norm);
-    return ddplm::launch(fn, a, norm_type == DDP_NORM_INF, true, stream);
+    return ddplm::launch(fn, a, norm_type == DDP_NORM_INF, stream);
 }

@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kRowTile = 256;   // rows of the gathered arrays are padded to this
 constexpr int kPrepThreads = 256;
-// G of one piece of the vocabulary, times two: 2^26 elements are 134 MB each
-constexpr int64_t kPieceElements = int64_t{1} << 26;
+// elements of G that are held at a time: 268 MB
+constexpr int64_t kPieceElements = int64_t{1} << 27;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // G's scale in fp16: its largest magnitude, 1 after the division by the largest
@@ -57,8 +57,9 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     s.dpad = round_up(D, 8);
     s.ntiles = (V + 127) / 128;  // one pair of statistics a row for each 128 words
     const int64_t vpad = round_up(V, 256);
-    if (piece <= 0) piece = std::max<int64_t>(1024, kPieceElements / s.tpad);
-    s.piece = std::min(vpad, round_up(piece, 256));
+    // G in two buffers of half the words asked for, one filled while the other is read
+    if (piece <= 0) piece = std::max<int64_t>(2048, kPieceElements / s.tpad);
+    s.piece = piece >= vpad ? vpad : std::min(vpad, round_up(piece, 512) / 2);
     s.pieces = backward ? (V + s.piece - 1) / s.piece : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -68,7 +69,7 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     };
     s.count = take(4);
     s.gmax = take(4);
-    s.next = take(4 * (s.pieces + 1));
+    s.next = take(4 * (vpad / 256 + 1));  // a counter for each launch: pieces + 1 at most
     s.rows = take(4 * s.tpad);
     s.target = take(4 * s.tpad);
     s.hidden = take(2 * s.tpad * s.dpad);
@@ -76,7 +77,7 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
         s.ratio = take(4 * s.tpad);
         s.lse = take(4 * s.tpad);
         s.grad_bytes = round_up(2 * s.tpad * s.piece, 256);
-        s.grad = take(s.grad_bytes * std::min<int64_t>(s.pieces, 2));  // one is filled while the other is read
+        s.grad = take(s.grad_bytes * std::min<int64_t>(s.pieces, 2));
         // splits x rows: at most (kSplitTiles / nt + mt) tiles of rows
         const int64_t nt = (D + 255) / 256;
         s.acc = take(4 * s.dpad * (s.tpad + kRowTile * ((kSplitTiles + nt - 1) / nt)));

@@ -6,63 +6,64 @@ and forwards to the library, which does all of the work.  Calls run on `stream`
 (default: torch's current stream).  Scratch memory is taken from torch's
 allocator for the length of a call, on the stream that the call runs on, and so
 are outputs that the caller does not pass.
+
+The smallest calls take a few microseconds on the GPU, so little is done on the
+way there: attributes are read once, and addresses go to the library as integers.
 """
 from __future__ import annotations
 
 import math
 
 import numpy as np
+import torch
 
-from . import (DDP_BF16, DDP_CLIP_WORKSPACE_BYTES, DDP_F16, DDP_F32, DDP_NORM_INF, DDP_NORM_L2, ddp_clip_grads,
-               ddp_embedding_backward, ddp_embedding_forward, ddp_embedding_workspace, ddp_grad_norm,
-               ddp_vocab_loss_backward, ddp_vocab_loss_forward, ddp_vocab_loss_workspace)
+from . import (DDP_BF16, DDP_CLIP_WORKSPACE_BYTES, DDP_F16, DDP_F32, DDP_NORM_INF, DDP_NORM_L2, _check, lib,
+               ddp_embedding_workspace, ddp_vocab_loss_workspace)
+
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:  # pragma: no cover - another torch
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+_DTYPES = {torch.float32: DDP_F32, torch.bfloat16: DDP_BF16, torch.float16: DDP_F16}
 
 
 def _dtype(t) -> int:
-    import torch
-
     try:
-        return {torch.float32: DDP_F32, torch.bfloat16: DDP_BF16, torch.float16: DDP_F16}[t]
+        return _DTYPES[t]
     except KeyError:
         raise ValueError(f"dtype {t} is not float32, bfloat16 or float16") from None
 
 
-def _on(stream):
-    """Allocations and the call on the same stream."""
-    import contextlib
-
-    import torch
-
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _raw(stream, device) -> int:
-    import torch
-
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-def _rows(x, name, rows, dim, dtypes):
-    """x as a [rows, dim] matrix with contiguous rows; its row stride."""
+def _rows(x, name, rows, dim, dtypes) -> int:
+    """x as a [rows, dim] matrix with contiguous rows on the GPU; its row stride."""
     if x.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {x.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if not x.is_cuda:
         raise ValueError(f"{name} is not on the GPU")
-    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != dim or (dim > 1 and x.stride(1) != 1) or \
-            (rows > 1 and x.stride(0) < dim):
-        raise ValueError(f"{name} must be [{rows}, {dim}] with contiguous rows, got shape {tuple(x.shape)} and "
-                         f"strides {x.stride()}")
-    return x.stride(0) if rows > 1 else dim
+    if x.dim() == 2:
+        r, c = x.shape
+        s, one = x.stride()
+        if r == rows and c == dim and (one == 1 or dim == 1) and (s >= dim or rows <= 1):
+            return s if rows > 1 else dim
+    raise ValueError(f"{name} must be [{rows}, {dim}] with contiguous rows, got shape {tuple(x.shape)} and "
+                     f"strides {x.stride()}")
 
 
-def _ids(x, name):
-    import torch
-
-    if x.dtype not in (torch.int64, torch.int32) or not x.is_cuda:
+def _ids(x, name) -> int:
+    """Bytes of an id."""
+    size = {torch.int64: 8, torch.int32: 4}.get(x.dtype)
+    if size is None or not x.is_cuda:
         raise ValueError(f"{name} must be int32 or int64 on the GPU")
     if x.dim() != 1 or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector, got shape {tuple(x.shape)}")
-    return x.element_size()
+    return size
+
+
+def _floats(x, name) -> None:
+    if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor on the GPU")
 
 
 class GradClipper:
@@ -76,8 +77,6 @@ class GradClipper:
     """
 
     def __init__(self, grads, out=None, norm_type=2.0):
-        import torch
-
         if norm_type not in (2, 2.0, math.inf):
             raise ValueError(f"norm_type {norm_type} is neither 2 nor inf")
         self.norm_type = DDP_NORM_INF if norm_type == math.inf else DDP_NORM_L2
@@ -96,50 +95,52 @@ class GradClipper:
             if o is not None and (o.dtype != g.dtype or o.numel() != g.numel() or not o.is_cuda
                                   or not o.is_contiguous()):
                 raise ValueError(f"output {k} is not a contiguous {g.dtype} tensor of {g.numel()} elements on the GPU")
-        dev = given[0].device if given else torch.device("cuda")
+        self.device = given[0].device if given else torch.device("cuda", torch.cuda.current_device())
         self._tensors = (grads, out)   # the pointer tables below point into these
         n = [0 if g is None else g.numel() for g in grads]
         off = np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
         self.total, self.ntensors = int(off[-1]), len(grads)
 
         def table(ts):
-            return torch.from_numpy(np.array([0 if t is None else t.data_ptr() for t in ts] or [0], np.int64)).to(dev)
+            return np.array([0 if t is None else t.data_ptr() for t in ts], np.int64)
 
-        self.grads_tab = table(grads)
-        self.out_tab = None if out is None else table(out)
-        self.offset = torch.from_numpy(off).to(dev)
-        self.dtypes = torch.from_numpy(np.array([DDP_F32 if g is None else _dtype(g.dtype) for g in grads] or [0],
-                                                np.int32)).to(dev)
-        self.device = dev
+        # one device buffer: offsets, addresses, the outputs' addresses, types
+        types = np.array([DDP_F32 if g is None else _dtype(g.dtype) for g in grads] + [0] * (len(grads) & 1), np.int32)
+        parts = [off, table(grads), table(out or []), types.view(np.int64)]
+        self._tables = torch.from_numpy(np.concatenate(parts)).to(self.device)
+        at = self._tables.data_ptr() + 8 * np.cumsum([0] + [len(p) for p in parts])
+        self.offset, self.grads_tab, out_tab, self.dtypes = (int(a) for a in at[:4])
+        self.out_tab = None if out is None else out_tab
 
     @classmethod
     def of_reducer(cls, reducer, w=0, norm_type=2.0):
         """Over replica w's reduced gradients: the views of a BucketReducer's main_grad."""
         return cls([reducer.view(p, w) for p in range(reducer.plan.nparams)], norm_type=norm_type)
 
-    def _call(self, clip, max_norm, stream):
-        import torch
-
-        with _on(stream):
-            norm = torch.empty(1, dtype=torch.float32, device=self.device)
-            ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
-            if clip:
-                ddp_clip_grads(self.grads_tab, self.out_tab, self.offset, self.dtypes, self.ntensors, self.total,
-                               self.norm_type, float(max_norm), norm, ws, DDP_CLIP_WORKSPACE_BYTES,
-                               _raw(stream, self.device))
-            else:
-                ddp_grad_norm(self.grads_tab, self.offset, self.dtypes, self.ntensors, self.total, self.norm_type,
-                              norm, ws, DDP_CLIP_WORKSPACE_BYTES, _raw(stream, self.device))
-        return norm
-
     def norm(self, stream=None):
         """The global norm, as a one-element tensor."""
-        return self._call(False, 0.0, stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.norm()
+        norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
+        _check(lib().ddp_grad_norm(self.grads_tab, self.offset, self.dtypes, self.ntensors, self.total, self.norm_type,
+                                   norm.data_ptr(), ws.data_ptr(), DDP_CLIP_WORKSPACE_BYTES,
+                                   _raw_stream(self.device.index)))
+        return norm
 
     def clip(self, max_norm, stream=None):
         """Scale the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm
         before clipping, as a one-element tensor."""
-        return self._call(True, max_norm, stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.clip(max_norm)
+        norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
+        _check(lib().ddp_clip_grads(self.grads_tab, self.out_tab, self.offset, self.dtypes, self.ntensors, self.total,
+                                    self.norm_type, max_norm, norm.data_ptr(), ws.data_ptr(),
+                                    DDP_CLIP_WORKSPACE_BYTES, _raw_stream(self.device.index)))
+        return norm
 
 
 class TokenEmbedding:
@@ -149,40 +150,47 @@ class TokenEmbedding:
         self.vocab, self.dim, self.torch_dtype, self.dtype = int(vocab), int(dim), dtype, _dtype(dtype)
         self.scale = float(scale)
         self.padding_idx = -1 if padding_idx is None else int(padding_idx)
+        self._same = (dtype,)
+        self._wide = (dtype, torch.float32)
 
     def forward(self, weight, ids, out=None, stream=None):
         """out[t] = scale * weight[ids[t]], a [tokens, dim] tensor."""
-        import torch
-
-        n = ids.numel()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(weight, ids, out)
+        n, dim = ids.numel(), self.dim
         id_bytes = _ids(ids, "ids")
-        ws = _rows(weight, "weight", self.vocab, self.dim, (self.torch_dtype,))
-        with _on(stream):
-            if out is None:
-                out = torch.empty((n, self.dim), dtype=self.torch_dtype, device=weight.device)
-            ddp_embedding_forward(weight, ws, self.dtype, self.vocab, self.dim, ids, id_bytes, n, self.scale, out,
-                                  _rows(out, "out", n, self.dim, (self.torch_dtype,)), _raw(stream, weight.device))
+        ws = _rows(weight, "weight", self.vocab, dim, self._same)
+        if out is None:
+            out, stride = torch.empty((n, dim), dtype=self.torch_dtype, device=weight.device), dim
+        else:
+            stride = _rows(out, "out", n, dim, self._same)
+        _check(lib().ddp_embedding_forward(weight.data_ptr(), ws, self.dtype, self.vocab, dim, ids.data_ptr(), id_bytes,
+                                           n, self.scale, out.data_ptr(), stride, _raw_stream(weight.get_device())))
         return out
 
     def backward(self, grad_out, ids, grad_weight=None, accumulate=False, stream=None):
         """The gradient of the table, [vocab, dim]; with accumulate it is added to
         grad_weight (of dtype, or float32: a main_grad view)."""
-        import torch
-
-        n = ids.numel()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(grad_out, ids, grad_weight, accumulate)
+        n, dim = ids.numel(), self.dim
         id_bytes = _ids(ids, "ids")
-        gs = _rows(grad_out, "grad_out", n, self.dim, (self.torch_dtype,))
-        with _on(stream):
-            if grad_weight is None:
-                if accumulate:
-                    raise ValueError("accumulate needs a grad_weight")
-                grad_weight = torch.empty((self.vocab, self.dim), dtype=self.torch_dtype, device=grad_out.device)
-            gws = _rows(grad_weight, "grad_weight", self.vocab, self.dim, (self.torch_dtype, torch.float32))
-            size = ddp_embedding_workspace(n, self.vocab, self.dim)
-            ws = torch.empty(size, dtype=torch.uint8, device=grad_out.device)
-            ddp_embedding_backward(grad_out, gs, self.dtype, ids, id_bytes, n, self.scale, self.padding_idx,
-                                   self.vocab, self.dim, grad_weight, gws, _dtype(grad_weight.dtype), accumulate, ws,
-                                   size, _raw(stream, grad_out.device))
+        gs = _rows(grad_out, "grad_out", n, dim, self._same)
+        if grad_weight is None:
+            if accumulate:
+                raise ValueError("accumulate needs a grad_weight")
+            grad_weight = torch.empty((self.vocab, dim), dtype=self.torch_dtype, device=grad_out.device)
+            gws = dim
+        else:
+            gws = _rows(grad_weight, "grad_weight", self.vocab, dim, self._wide)
+        size = ddp_embedding_workspace(n, self.vocab, dim)
+        ws = torch.empty(size, dtype=torch.uint8, device=grad_out.device)
+        _check(lib().ddp_embedding_backward(grad_out.data_ptr(), gs, self.dtype, ids.data_ptr(), id_bytes, n, self.scale,
+                                            self.padding_idx, self.vocab, dim, grad_weight.data_ptr(), gws,
+                                            _DTYPES[grad_weight.dtype], int(accumulate), ws.data_ptr(), size,
+                                            _raw_stream(grad_out.get_device())))
         return grad_weight
 
 
@@ -199,36 +207,31 @@ class VocabLoss:
         if self.dtype == DDP_F32:
             raise ValueError("the vocabulary loss takes bfloat16 or float16 inputs")
         self.ignore_index, self.piece = int(ignore_index), int(piece)
-        self._sizes = {}
-
-    def _workspace(self, n, weight, ws):
-        aligned = weight.data_ptr() % 16 == 0 and ws % 8 == 0
-        key = (n, aligned)
-        if key not in self._sizes:
-            if len(self._sizes) > 64:
-                self._sizes.clear()
-            self._sizes[key] = ddp_vocab_loss_workspace(n, self.vocab, self.dim, self.piece, aligned)
-        return self._sizes[key]
+        self._same = (dtype,)
+        self._wide = (dtype, torch.float32)
 
     def _inputs(self, hidden, weight, targets):
         n = targets.numel()
         id_bytes = _ids(targets, "targets")
-        hs = _rows(hidden, "hidden", n, self.dim, (self.torch_dtype,))
-        ws = _rows(weight, "weight", self.vocab, self.dim, (self.torch_dtype,))
-        return n, id_bytes, hs, ws
+        hs = _rows(hidden, "hidden", n, self.dim, self._same)
+        ws = _rows(weight, "weight", self.vocab, self.dim, self._same)
+        at = weight.data_ptr()
+        sizes = ddp_vocab_loss_workspace(n, self.vocab, self.dim, self.piece, at % 16 == 0 and ws % 8 == 0)
+        return n, id_bytes, hs, ws, at, sizes
 
     def forward(self, hidden, weight, targets, stream=None):
         """(loss, lse) of each token, float32; both 0 where the target is ignore_index."""
-        import torch
-
-        n, id_bytes, hs, ws = self._inputs(hidden, weight, targets)
-        size = self._workspace(n, weight, ws)[0]
-        with _on(stream):
-            both = torch.empty((2, n), dtype=torch.float32, device=weight.device)
-            scratch = torch.empty(size, dtype=torch.uint8, device=weight.device)
-            loss, lse = both[0], both[1]
-            ddp_vocab_loss_forward(hidden, hs, weight, ws, self.dtype, n, self.vocab, self.dim, targets, id_bytes,
-                                   self.ignore_index, loss, lse, scratch, size, _raw(stream, weight.device))
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(hidden, weight, targets)
+        n, id_bytes, hs, ws, at, (size, _) = self._inputs(hidden, weight, targets)
+        both = torch.empty((2, n), dtype=torch.float32, device=weight.device)
+        scratch = torch.empty(size, dtype=torch.uint8, device=weight.device)
+        loss, lse = both.unbind(0)
+        _check(lib().ddp_vocab_loss_forward(hidden.data_ptr(), hs, at, ws, self.dtype, n, self.vocab, self.dim,
+                                            targets.data_ptr(), id_bytes, self.ignore_index, loss.data_ptr(),
+                                            lse.data_ptr(), scratch.data_ptr(), size,
+                                            _raw_stream(weight.get_device())))
         return loss, lse
 
     def backward(self, hidden, weight, targets, lse, grad_loss, grad_hidden=None, grad_weight=None, accumulate=False,
@@ -237,33 +240,42 @@ class VocabLoss:
         one value a token, or one value for all of them.  With accumulate the
         weight's gradient is added to grad_weight (of dtype, or float32: a
         main_grad view)."""
-        import torch
-
-        n, id_bytes, hs, ws = self._inputs(hidden, weight, targets)
-        for x, name in ((lse, "lse"), (grad_loss, "grad_loss")):
-            if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 tensor on the GPU")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight, accumulate,
+                                     need_hidden, need_weight)
+        n, id_bytes, hs, ws, at, (_, size) = self._inputs(hidden, weight, targets)
+        _floats(lse, "lse")
+        _floats(grad_loss, "grad_loss")
         if lse.numel() != n:
             raise ValueError(f"lse has {lse.numel()} elements for {n} tokens")
         if grad_loss.numel() not in (1, n):
             raise ValueError(f"grad_loss has {grad_loss.numel()} elements for {n} tokens")
-        size = self._workspace(n, weight, ws)[1]
-        with _on(stream):
-            ghs = gws = self.dim
-            if need_hidden:
-                if grad_hidden is None:
-                    grad_hidden = torch.empty((n, self.dim), dtype=self.torch_dtype, device=weight.device)
-                ghs = _rows(grad_hidden, "grad_hidden", n, self.dim, (self.torch_dtype,))
-            if need_weight:
-                if grad_weight is None:
-                    if accumulate:
-                        raise ValueError("accumulate needs a grad_weight")
-                    grad_weight = torch.empty((self.vocab, self.dim), dtype=self.torch_dtype, device=weight.device)
-                gws = _rows(grad_weight, "grad_weight", self.vocab, self.dim, (self.torch_dtype, torch.float32))
-            scratch = torch.empty(size, dtype=torch.uint8, device=weight.device)
-            ddp_vocab_loss_backward(hidden, hs, weight, ws, self.dtype, n, self.vocab, self.dim, targets, id_bytes,
-                                    self.ignore_index, lse, grad_loss, int(grad_loss.numel() == n and n != 1),
-                                    grad_hidden if need_hidden else None, ghs, grad_weight if need_weight else None,
-                                    gws, _dtype(grad_weight.dtype) if need_weight else self.dtype, accumulate,
-                                    self.piece, scratch, size, _raw(stream, weight.device))
-        return (grad_hidden if need_hidden else None), (grad_weight if need_weight else None)
+        dim = ghs = gws = self.dim
+        if not need_hidden:
+            grad_hidden = None
+        elif grad_hidden is None:
+            grad_hidden = torch.empty((n, dim), dtype=self.torch_dtype, device=weight.device)
+        else:
+            ghs = _rows(grad_hidden, "grad_hidden", n, dim, self._same)
+        if not need_weight:
+            grad_weight = None
+        elif grad_weight is None:
+            if accumulate:
+                raise ValueError("accumulate needs a grad_weight")
+            grad_weight = torch.empty((self.vocab, dim), dtype=self.torch_dtype, device=weight.device)
+        else:
+            gws = _rows(grad_weight, "grad_weight", self.vocab, dim, self._wide)
+        scratch = torch.empty(size, dtype=torch.uint8, device=weight.device)
+        # an empty output has no address; the library takes NULL for "not wanted"
+        if grad_hidden is not None and n == 0 and grad_weight is None:
+            return grad_hidden, None
+        _check(lib().ddp_vocab_loss_backward(hidden.data_ptr(), hs, at, ws, self.dtype, n, self.vocab, dim,
+                                             targets.data_ptr(), id_bytes, self.ignore_index, lse.data_ptr(),
+                                             grad_loss.data_ptr(), int(grad_loss.numel() == n and n != 1),
+                                             None if grad_hidden is None else grad_hidden.data_ptr(), ghs,
+                                             None if grad_weight is None else grad_weight.data_ptr(), gws,
+                                             self.dtype if grad_weight is None else _DTYPES[grad_weight.dtype],
+                                             int(accumulate), self.piece, scratch.data_ptr(), size,
+                                             _raw_stream(weight.get_device())))
+        return grad_hidden, grad_weight

@@ -965,7 +965,8 @@ ddp_status ddp_embedding_backward(const void* grad_out, int64_t grad_stride, int
 /*
  * Workspace of the vocabulary loss in bytes.  piece: vocabulary words whose
  * softmax gradient is held at a time by the backward pass (rounded up to a
- * multiple of 256); 0: the library's choice.  weight_aligned: nonzero if the
+ * multiple of 512; the passes over the vocabulary take half of them each); 0: the
+ * library's choice.  weight_aligned: nonzero if the
  * weight starts on a 16-byte boundary and its row stride is a multiple of 8
  * elements; otherwise the calls work on an aligned copy in the workspace.
  * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, NULL outputs).
