@@ -3,7 +3,7 @@
 //   n = sqrt(sum_k sum_i g_k[i]^2)  or  max |g_k[i]|,   c = min(1, max_norm / (n + 1e-6)),   g_k[i] <- c g_k[i]
 //
 // The tensors are laid end to end in one element space (their lengths' prefix
-// sums).  A CTA takes a contiguous slice of it, its warps take turns of kTurn elements,
+// sums).  A CTA takes a contiguous slice of it, its warps take turns of some elements,
 // and each walks the tensors in its turn by itself, so that hundreds of small tensors
 // cost neither more launches nor a wait for each.
 //
@@ -22,15 +22,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerSm = 3;        // CTAs of the two passes on an SM
-constexpr int kTurn = 2048;      // elements of a warp's turn: 16 (fp32) or 8 vectors a lane
-constexpr int kBatch = 4;        // vectors a lane keeps in flight (two in the cluster, whose threads have fewer registers)
+constexpr int kBatch = 4;        // vectors a lane keeps in flight
 constexpr int kWindow = kThreads;  // tensors whose tables a CTA holds at a time
 constexpr int kMaxGrid = DDP_CLIP_WORKSPACE_BYTES / 8;  // one double of partial result a CTA
-// Up to here one cluster of 16 CTAs does both passes: the norm crosses its shared memory
-// instead of a second launch.
-constexpr int64_t kClusterElements = 400000;
-constexpr int kClusterCtas = 16;
-constexpr int kClusterThreads = 1024;
 
 struct ClipArgs {
     const void* const* grads;
@@ -43,6 +37,7 @@ struct ClipArgs {
     float* norm;
     float max_norm;
     int32_t clip;
+    int32_t turn;  // elements of a warp's turn (set by the launcher)
 };
 
 // A CTA's view of the tables: `count` tensors from `first`.
@@ -86,7 +81,7 @@ __device__ __forceinline__ int find_tensor(const ClipArgs& a, int64_t e)
 }
 
 // A value's square is exact enough in fp32 while it stays well inside its range:
-// values whose largest magnitude lies outside [2^-40, 2^60] are squared in fp64.
+// values whose largest magnitude lies outside [2^-40, 2^60] are scaled first.
 __device__ __forceinline__ bool fp32_square_range(float m) { return m >= 0x1p-40f && m <= 0x1p60f; }
 
 // larger magnitude where a NaN beats everything
@@ -121,8 +116,13 @@ template <bool INF, int N> __device__ __forceinline__ void add_values(double& ac
     if (fp32_square_range(m)) {
         acc += static_cast<double>(s0 + s1);
     } else if (!(s0 + s1 == 0.f && m == 0.f)) {
+        // moved into the range by a power of two, whose square is taken out again in fp64
+        const bool large = m > 1.f;
+        const float f = large ? 0x1p-68f : 0x1p100f;
+        s0 = 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc = fma(static_cast<double>(x[j]), static_cast<double>(x[j]), acc);
+        for (int j = 0; j < N; ++j) s0 = fmaf(x[j] * f, x[j] * f, s0);
+        acc += static_cast<double>(s0) * (large ? 0x1p136 : 0x1p-200);
     }
 }
 
@@ -146,8 +146,8 @@ template <typename T> __device__ __forceinline__ int head_of(const T* p, int n)
     return min(n, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T)));
 }
 
-// one warp, n <= kTurn values of one tensor
-template <int DT, bool INF, int B> __device__ __forceinline__ void norm_piece(const void* base, int64_t i0, int n, int lane, double& acc)
+// one warp, n values (a turn's or fewer) of one tensor
+template <int DT, bool INF> __device__ __forceinline__ void norm_piece(const void* base, int64_t i0, int n, int lane, double& acc)
 {
     using T = typename Elem<DT>::T;
     constexpr int N = Vec<DT>::N;
@@ -157,13 +157,13 @@ template <int DT, bool INF, int B> __device__ __forceinline__ void norm_piece(co
     float e[2] = {lane < head ? Elem<DT>::to_f(p[lane]) : 0.f, tail + lane < n ? Elem<DT>::to_f(p[tail + lane]) : 0.f};
     const Vec<DT>* pv = reinterpret_cast<const Vec<DT>*>(p + head);
     int i = lane;
-    for (; i + 32 * (B - 1) < nv; i += 32 * B) {
-        Vec<DT> v[B];
+    for (; i + 32 * (kBatch - 1) < nv; i += 32 * kBatch) {
+        Vec<DT> v[kBatch];
 #pragma unroll
-        for (int u = 0; u < B; ++u) v[u] = pv[i + 32 * u];
-        float x[B * N];
+        for (int u = 0; u < kBatch; ++u) v[u] = pv[i + 32 * u];
+        float x[kBatch * N];
 #pragma unroll
-        for (int u = 0; u < B; ++u)
+        for (int u = 0; u < kBatch; ++u)
 #pragma unroll
             for (int j = 0; j < N; ++j) x[u * N + j] = Elem<DT>::to_f(v[u].v[j]);
         add_values<INF>(acc, x);
@@ -178,7 +178,7 @@ template <int DT, bool INF, int B> __device__ __forceinline__ void norm_piece(co
     add_values<INF>(acc, e);
 }
 
-template <int DT, int B> __device__ __forceinline__ void scale_piece(const void* src, void* dst, int64_t i0, int n, int lane, float c)
+template <int DT> __device__ __forceinline__ void scale_piece(const void* src, void* dst, int64_t i0, int n, int lane, float c)
 {
     using T = typename Elem<DT>::T;
     constexpr int N = Vec<DT>::N;
@@ -186,13 +186,13 @@ template <int DT, int B> __device__ __forceinline__ void scale_piece(const void*
     T* q = static_cast<T*>(dst) + i0;
     if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) {
         // vectors need both sides at the same place within 16 bytes
-        for (int i = lane; i < n; i += 32 * B) {
-            T v[B];
+        for (int i = lane; i < n; i += 32 * kBatch) {
+            T v[kBatch];
 #pragma unroll
-            for (int u = 0; u < B; ++u)
+            for (int u = 0; u < kBatch; ++u)
                 if (i + 32 * u < n) v[u] = p[i + 32 * u];
 #pragma unroll
-            for (int u = 0; u < B; ++u)
+            for (int u = 0; u < kBatch; ++u)
                 if (i + 32 * u < n) q[i + 32 * u] = Elem<DT>::from_f(Elem<DT>::to_f(v[u]) * c);
         }
         return;
@@ -202,13 +202,13 @@ template <int DT, int B> __device__ __forceinline__ void scale_piece(const void*
     if (tail + lane < n) q[tail + lane] = Elem<DT>::from_f(Elem<DT>::to_f(p[tail + lane]) * c);
     const Vec<DT>* pv = reinterpret_cast<const Vec<DT>*>(p + head);
     Vec<DT>* qv = reinterpret_cast<Vec<DT>*>(q + head);
-    for (int i = lane; i < nv; i += 32 * B) {
-        Vec<DT> v[B];
+    for (int i = lane; i < nv; i += 32 * kBatch) {
+        Vec<DT> v[kBatch];
 #pragma unroll
-        for (int u = 0; u < B; ++u)
+        for (int u = 0; u < kBatch; ++u)
             if (i + 32 * u < nv) v[u] = pv[i + 32 * u];
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
+        for (int u = 0; u < kBatch; ++u) {
             if (i + 32 * u >= nv) continue;
 #pragma unroll
             for (int j = 0; j < N; ++j) v[u].v[j] = Elem<DT>::from_f(Elem<DT>::to_f(v[u].v[j]) * c);
@@ -219,24 +219,24 @@ template <int DT, int B> __device__ __forceinline__ void scale_piece(const void*
 }
 
 // What a walk over the elements does with a piece of a tensor.
-template <bool INF, int B> struct NormWalk {
+template <bool INF> struct NormWalk {
     double acc = 0.0;
     template <int N> __device__ __forceinline__ void piece(const Window<N>& w, int k, int64_t i0, int n, int lane)
     {
         if (!w.grad[k]) return;
-        if (w.dtype[k] == DDP_F32) norm_piece<DDP_F32, INF, B>(w.grad[k], i0, n, lane, acc);
-        else if (w.dtype[k] == DDP_BF16) norm_piece<DDP_BF16, INF, B>(w.grad[k], i0, n, lane, acc);
-        else norm_piece<DDP_F16, INF, B>(w.grad[k], i0, n, lane, acc);
+        if (w.dtype[k] == DDP_F32) norm_piece<DDP_F32, INF>(w.grad[k], i0, n, lane, acc);
+        else if (w.dtype[k] == DDP_BF16) norm_piece<DDP_BF16, INF>(w.grad[k], i0, n, lane, acc);
+        else norm_piece<DDP_F16, INF>(w.grad[k], i0, n, lane, acc);
     }
 };
-template <int B> struct ScaleWalk {
+struct ScaleWalk {
     float c;
     template <int N> __device__ __forceinline__ void piece(const Window<N>& w, int k, int64_t i0, int n, int lane)
     {
         if (!w.grad[k] || !w.out[k]) return;
-        if (w.dtype[k] == DDP_F32) scale_piece<DDP_F32, B>(w.grad[k], w.out[k], i0, n, lane, c);
-        else if (w.dtype[k] == DDP_BF16) scale_piece<DDP_BF16, B>(w.grad[k], w.out[k], i0, n, lane, c);
-        else scale_piece<DDP_F16, B>(w.grad[k], w.out[k], i0, n, lane, c);
+        if (w.dtype[k] == DDP_F32) scale_piece<DDP_F32>(w.grad[k], w.out[k], i0, n, lane, c);
+        else if (w.dtype[k] == DDP_BF16) scale_piece<DDP_BF16>(w.grad[k], w.out[k], i0, n, lane, c);
+        else scale_piece<DDP_F16>(w.grad[k], w.out[k], i0, n, lane, c);
     }
 };
 
@@ -244,9 +244,9 @@ template <int B> struct ScaleWalk {
 // end where BACK.  The window holds the tensors of the slice; where it does not hold all
 // of them the slice is walked in parts, a window each.
 template <bool BACK, typename F, int N>
-__device__ __forceinline__ void walk(Window<N>& w, const ClipArgs& a, int first, int64_t e0, int64_t e1, int turn, F& f)
+__device__ __forceinline__ void walk(Window<N>& w, const ClipArgs& a, int first, int64_t e0, int64_t e1, F& f)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, turn = a.turn;
     if (w.first != first) load_window(w, a, first);
     for (int64_t s0 = e0; s0 < e1;) {
         const int64_t s1 = min(e1, w.offset[w.count]);
@@ -293,10 +293,10 @@ template <bool INF> __global__ void __launch_bounds__(kThreads, kPerSm) norm_ker
     allow_next();
     int64_t e0, e1;
     slice_of(a, blockIdx.x, gridDim.x, &e0, &e1);
-    NormWalk<INF, kBatch> f;
+    NormWalk<INF> f;
     if (threadIdx.x == 0) w.first = -1;
     __syncthreads();
-    if (e0 < e1) walk<false>(w, a, a.ntensors <= kWindow ? 0 : find_tensor(a, e0), e0, e1, kTurn, f);
+    if (e0 < e1) walk<false>(w, a, a.ntensors <= kWindow ? 0 : find_tensor(a, e0), e0, e1, f);
     const double r = block_join<INF>(f.acc);
     if (threadIdx.x == 0) a.part[blockIdx.x] = r;
 }
@@ -331,49 +331,24 @@ template <bool INF> __global__ void __launch_bounds__(kThreads, kPerSm) scale_ke
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
     const float c = factor(a, norm);
     if (e0 >= e1 || (c == 1.f && !a.out)) return;
-    ScaleWalk<kBatch> f{c};
-    walk<true>(w, a, first, e0, e1, kTurn, f);
+    ScaleWalk f{c};
+    walk<true>(w, a, first, e0, e1, f);
 }
 
-// Both passes by one cluster: the CTAs' partial results cross its shared memory, and the
-// second pass finds the elements in L1 or L2.
-template <bool INF> __global__ void __launch_bounds__(kClusterThreads) cluster_kernel(const __grid_constant__ ClipArgs a)
+// Elements of a warp's turn, a multiple of 256.  Long turns keep a lane's loads in batches
+// (124M bf16 elements: 171 us with 2048, 156 with 4096, 158 with 8192); few elements
+// are spread over the machine's warps (1M elements: 21.5 us with 2048, 24.6 with 4096).
+constexpr int kMaxTurn = 4096;
+int turn_for(int64_t total)
 {
-    __shared__ Window<kWindow> w;
-    __shared__ double parts[kClusterCtas];
-    int64_t e0, e1;
-    slice_of(a, blockIdx.x, gridDim.x, &e0, &e1);
-    const int turn = static_cast<int>(((e1 - e0) / (kClusterThreads / 32) + 256) / 256 * 256);
-    if (threadIdx.x == 0) w.first = -1;
-    __syncthreads();
-    wait_for_previous();
-    const int first = e0 < e1 && a.ntensors > kWindow ? find_tensor(a, e0) : 0;
-    NormWalk<INF, 2> f;
-    if (e0 < e1) walk<false>(w, a, first, e0, e1, turn, f);
-    const double r = block_join<INF>(f.acc);
-    if (threadIdx.x < gridDim.x) {
-        uint32_t at;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;"
-            : "=r"(at)
-            : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&parts[blockIdx.x]))), "r"(threadIdx.x));
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(r) : "memory");
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    double acc = 0.0;
-    for (int i = 0; i < static_cast<int>(gridDim.x); ++i) acc = join<INF>(acc, parts[i]);
-    const float norm = INF ? static_cast<float>(acc) : static_cast<float>(sqrt(acc));
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-    if (!a.clip) return;
-    const float c = factor(a, norm);
-    if (e0 >= e1 || (c == 1.f && !a.out)) return;
-    ScaleWalk<2> s{c};
-    walk<false>(w, a, first, e0, e1, turn, s);
+    const int64_t warps = static_cast<int64_t>(ddp::device_sm_count()) * kPerSm * kWarps;
+    return static_cast<int>(std::min<int64_t>(kMaxTurn, (total / warps + 256) / 256 * 256));
 }
 
 // one wave of CTAs at most, a turn for each warp at least
-int grid_for(int64_t total)
+int grid_for(int64_t total, int turn)
 {
-    const int64_t want = (total + kTurn * kWarps - 1) / (kTurn * kWarps);
+    const int64_t want = (total + turn * kWarps - 1) / (turn * kWarps);
     const int64_t wave = static_cast<int64_t>(ddp::device_sm_count()) * kPerSm;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, wave, kMaxGrid})));
 }
@@ -396,44 +371,9 @@ ddp_status check(const char* fn, const ClipArgs& a, int32_t norm_type, const voi
     return DDP_OK;
 }
 
-template <bool INF> cudaError_t launch_cluster(const ClipArgs& a, cudaStream_t s)
-{
-    // 16 CTAs are more than every device promises to run as a cluster: asked for once a device
-    static std::atomic<int> cached[ddp::kMaxDevices] = {};
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kClusterThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    const int dev = ddp::current_device();
-    int ctas = dev >= 0 ? cached[dev].load(std::memory_order_relaxed) : 0;
-    if (!ctas) {
-        cudaError_t e = cudaFuncSetAttribute(cluster_kernel<INF>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        int n = 0;
-        cfg.numAttrs = 1;
-        for (ctas = kClusterCtas; ctas > 1; ctas /= 2) {
-            cfg.gridDim = dim3(ctas);
-            at[0].val.clusterDim.x = ctas;
-            if (cudaOccupancyMaxActiveClusters(&n, cluster_kernel<INF>, &cfg) == cudaSuccess && n > 0) break;
-        }
-        (void)cudaGetLastError();
-        if (dev >= 0) cached[dev].store(ctas, std::memory_order_relaxed);
-    }
-    cfg.gridDim = dim3(ctas);
-    at[0].val.clusterDim.x = ctas;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, cluster_kernel<INF>, a);
-}
-
 template <bool INF> cudaError_t launch_as(const ClipArgs& a, cudaStream_t s)
 {
-    if (a.total <= kClusterElements) return launch_cluster<INF>(a, s);
-    const dim3 grid(grid_for(a.total));
+    const dim3 grid(grid_for(a.total, a.turn));
     const cudaError_t e = launch_chained(norm_kernel<INF>, grid, kThreads, 0, s, a);
     if (e != cudaSuccess) return e;
     if (a.clip) return launch_chained(scale_kernel<INF>, grid, kThreads, 0, s, a);
@@ -441,8 +381,9 @@ template <bool INF> cudaError_t launch_as(const ClipArgs& a, cudaStream_t s)
                           static_cast<int>(grid.x), a.norm);
 }
 
-ddp_status launch(const char* fn, const ClipArgs& a, bool inf, void* stream)
+ddp_status launch(const char* fn, ClipArgs a, bool inf, void* stream)
 {
+    a.turn = turn_for(a.total);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t err = inf ? launch_as<true>(a, s) : launch_as<false>(a, s);
     if (err != cudaSuccess) return ddp::fail(DDP_E_CUDA, "%s: kernel launch failed: %s", fn, cudaGetErrorString(err));
@@ -456,7 +397,7 @@ extern "C" ddp_status ddp_grad_norm(const void* const* grads, const int64_t* off
                                     int32_t ntensors, int64_t total, int32_t norm_type, float* norm, void* workspace,
                                     int64_t workspace_bytes, void* stream)
 {
-    const ddplm::ClipArgs a{grads, nullptr, offset, dtypes, ntensors, total, static_cast<double*>(workspace), norm, 0.f, 0};
+    const ddplm::ClipArgs a{grads, nullptr, offset, dtypes, ntensors, total, static_cast<double*>(workspace), norm, 0.f, 0, 0};
     const ddp_status st = ddplm::check("ddp_grad_norm", a, norm_type, workspace, workspace_bytes);
     if (st != DDP_OK) return st;
     return ddplm::launch("ddp_grad_norm", a, norm_type == DDP_NORM_INF, stream);
@@ -469,7 +410,7 @@ extern "C" ddp_status ddp_clip_grads(const void* const* grads, void* const* out,
 {
     const char* fn = "ddp_clip_grads";
     const ddplm::ClipArgs a{grads, out, offset, dtypes, ntensors, total, static_cast<double*>(workspace), norm,
-                            max_norm, 1};
+                            max_norm, 1, 0};
     const ddp_status st = ddplm::check(fn, a, norm_type, workspace, workspace_bytes);
     if (st != DDP_OK) return st;
     if (!(max_norm >= 0.f)) return ddp::fail(DDP_E_INVAL, "%s: max_norm = %g is negative or NaN", fn, max_norm);
