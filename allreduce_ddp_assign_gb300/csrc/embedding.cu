@@ -74,8 +74,10 @@ lookup_kernel(const void* weight, int64_t ws, int64_t vocab, int64_t dim, const 
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr uint16_t kNone = 0xffff;
 constexpr int kMaxRange = 1024;  // ids a sorting CTA owns at most (its counters: 4 bytes an id and warp)
-constexpr int kBatch = 8;        // loads a thread keeps in flight
+constexpr int kIdBatch = 8;      // loads of ids a thread keeps in flight
+constexpr int kSortSmem = 220 * 1024;  // counters, and the tokens' places in the range where they fit
 
 struct SortArgs {
     const void* ids;
@@ -87,6 +89,7 @@ struct SortArgs {
     int32_t* key;    // [ntokens] their ids
     int32_t* start;  // [vocab + 1] first place of each id in `order`
     int* status;
+    int32_t cached;  // the second pass reads what the first one left in shared memory
     // rows of ids that do not occur (nullptr: left alone)
     uint8_t* clear;
     int64_t clear_stride, clear_bytes;
@@ -99,31 +102,64 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
     __shared__ uint8_t seen[kMaxRange];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t* cnt = sh + warp * a.range;
+    uint16_t* place = reinterpret_cast<uint16_t*>(sh + kSortWarps * a.range);  // [ntokens], where it fits
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.range;
     const int64_t hi = lo + a.range < a.vocab ? lo + a.range : a.vocab;
     const int nr = static_cast<int>(hi - lo);
     for (int i = tid; i < kSortWarps * a.range; i += kSortThreads) sh[i] = 0;
     __syncthreads();
     wait_for_previous();
-    // each warp counts a contiguous stretch of tokens
-    const int per = (a.ntokens + kSortWarps - 1) / kSortWarps;
+    // An id relative to the range, as far as it is one of the range's; kNone: another's.
+    // (ids of 2^31 and more are out of any vocabulary)
+    const uint32_t lo32 = static_cast<uint32_t>(lo), vocab32 = static_cast<uint32_t>(a.vocab);
+    const uint32_t pad32 = a.padding_idx >= 0 && a.padding_idx < a.vocab ? static_cast<uint32_t>(a.padding_idx) : 0xffffffffu;
+    auto in_range = [&](int64_t id) {
+        const uint32_t x = static_cast<uint32_t>(id);
+        const bool good = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32 && x != pad32;
+        return good && x - lo32 < static_cast<uint32_t>(nr) ? static_cast<uint16_t>(x - lo32) : kNone;
+    };
+    // each warp counts a contiguous stretch of tokens (a multiple of 64 of them)
+    const int per = (a.ntokens + 64 * kSortWarps - 1) / (64 * kSortWarps) * 64;
     const int t0 = min(warp * per, a.ntokens), t1 = min(t0 + per, a.ntokens);
     int32_t less = 0;
-    for (int t = t0 + lane; t < t1; t += 32 * kBatch) {
-        int64_t id[kBatch];
+    bool bad = false;
+    auto count = [&](int t, int64_t id) {
+        const uint32_t x = static_cast<uint32_t>(id);
+        const bool known = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32;
+        bad |= !known;
+        const uint32_t r = x - lo32;
+        const bool counts = known && x != pad32;
+        less += counts && x < lo32;
+        const bool mine = counts && r < static_cast<uint32_t>(nr);
+        if (mine) atomicAdd(&cnt[r], 1);
+        if (a.cached) place[t] = mine ? static_cast<uint16_t>(r) : kNone;
+    };
+    // pairs of ids in 16-byte (8-byte) loads where the list starts on such a boundary
+    const bool pairs = (reinterpret_cast<uintptr_t>(a.ids) & (2 * a.id_bytes - 1)) == 0;
+    const int whole = pairs ? t0 + (t1 - t0) / 2 * 2 : t0;
+    for (int t = t0 + 2 * lane; t < whole; t += 64 * kIdBatch) {
+        int64_t id[kIdBatch][2];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) id[j] = t + 32 * j < t1 ? load_id(a.ids, a.id_bytes, t + 32 * j) : -1;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (t + 32 * j >= t1 || (a.padding_idx >= 0 && id[j] == a.padding_idx)) continue;
-            if (id[j] < 0 || id[j] >= a.vocab) {
-                if (blockIdx.x == 0) atomicOr(a.status, kErrId);
-                continue;
+        for (int j = 0; j < kIdBatch; ++j) {
+            const int u = t + 64 * j;
+            if (u >= whole) continue;
+            if (a.id_bytes == 8) {
+                const longlong2 v = __ldg(reinterpret_cast<const longlong2*>(static_cast<const long long*>(a.ids) + u));
+                id[j][0] = v.x; id[j][1] = v.y;
+            } else {
+                const int2 v = __ldg(reinterpret_cast<const int2*>(static_cast<const int*>(a.ids) + u));
+                id[j][0] = v.x; id[j][1] = v.y;
             }
-            less += id[j] < lo;
-            if (id[j] >= lo && id[j] < hi) atomicAdd(&cnt[static_cast<int>(id[j] - lo)], 1);
+        }
+#pragma unroll
+        for (int j = 0; j < kIdBatch; ++j) {
+            if (t + 64 * j >= whole) continue;
+            count(t + 64 * j, id[j][0]);
+            count(t + 64 * j + 1, id[j][1]);
         }
     }
+    for (int t = whole + lane; t < t1; t += 32) count(t, load_id(a.ids, a.id_bytes, t));
+    if (bad && blockIdx.x == 0) atomicOr(a.status, kErrId);
 #pragma unroll
     for (int o = 16; o; o >>= 1) less += __shfl_xor_sync(0xffffffffu, less, o);
     if (lane == 0) less_w[warp] = less;
@@ -157,22 +193,24 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
         }
     }
     __syncthreads();
-    for (int t = t0; t < t1; t += 32 * kBatch) {
-        int64_t id[kBatch];
+    for (int t = t0; t < t1; t += 32 * kIdBatch) {
+        uint16_t at_row[kIdBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            id[j] = t + 32 * j + lane < t1 ? load_id(a.ids, a.id_bytes, t + 32 * j + lane) : -1;
+        for (int j = 0; j < kIdBatch; ++j) {
+            const int u = t + 32 * j + lane;
+            at_row[j] = u >= t1 ? kNone : a.cached ? place[u] : in_range(load_id(a.ids, a.id_bytes, u));
+        }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const bool mine = id[j] >= lo && id[j] < hi && id[j] != a.padding_idx;
+        for (int j = 0; j < kIdBatch; ++j) {
+            const bool mine = at_row[j] != kNone;
             const uint32_t any = __ballot_sync(0xffffffffu, mine);
             if (!any) continue;
             if (mine) {
-                const int r = static_cast<int>(id[j] - lo);
+                const int r = at_row[j];
                 const uint32_t same = __match_any_sync(any, r);
                 const int at = cnt[r] + __popc(same & ((1u << lane) - 1u));
                 a.order[at] = t + 32 * j + lane;
-                a.key[at] = static_cast<int32_t>(id[j]);
+                a.key[at] = static_cast<int32_t>(lo32 + r);
                 __syncwarp(same);
                 if (lane == __ffs(same) - 1) cnt[r] += __popc(same);
             }
@@ -194,10 +232,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
 }
 
 // Runs of equal ids are cut into chunks of the sorted order, so that a frequent word's
-// run is summed by many warps.  A warp sums one chunk in 32 lanes' columns; runs that
-// lie within the chunk go to the table, a run's part that reaches over the chunk's
-// edge goes to the workspace: `head` of a chunk is the part of a run that began before
-// it, `tail` the part of one that begins in it and goes on.
+// run is summed by many warps.  A warp sums one chunk in one slab of columns; a CTA's
+// eight warps take eight chunks in a row, a block.  A run inside a chunk goes to the
+// table at once; a run's part that reaches over the chunk's edge stays in shared memory
+// until the block's parts are added, and what reaches over the block's edge goes to the
+// workspace: `head`, the part of a run that began before the block (chunk), and `tail`,
+// the part of one that begins in it and goes on.
 struct GradArgs {
     const void* g;
     int64_t gs;
@@ -206,7 +246,7 @@ struct GradArgs {
     const int32_t* start;
     int64_t vocab, dim;
     int32_t chunk;
-    float* edge;  // [chunks][head, tail][dim]
+    float* edge;  // [blocks][head, tail][dim]
     float scale;
     void* gw;
     int64_t ws;
@@ -221,18 +261,42 @@ template <int DT, bool VEC> struct Columns {
     {
         return slab * kSlab + (VEC ? lane * N + j : lane + 32 * j);
     }
-    __device__ __forceinline__ static void load(const void* g, int64_t row, int64_t dim, int64_t slab, int lane, float (&x)[N])
+    // A row's columns into a warp's slot of kSlotBytes; past the row's end, zeros.  VEC: an
+    // asynchronous copy, complete after copies_done().
+    static constexpr int kSlotBytes = 32 * N * static_cast<int>(sizeof(typename Elem<DT>::T));
+    __device__ __forceinline__ static void fetch(uint8_t* slot, const void* g, int64_t row, int64_t dim, int64_t slab, int lane)
     {
         using T = typename Elem<DT>::T;
         const T* p = static_cast<const T*>(g) + row;
         if (VEC) {
-            Vec<DT> v{};
-            if (at(slab, lane, 0) < dim) v = *reinterpret_cast<const Vec<DT>*>(p + at(slab, lane, 0));
+            const bool in = at(slab, lane, 0) < dim;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             static_cast<uint32_t>(__cvta_generic_to_shared(slot + lane * 16))),
+                         "l"(in ? p + at(slab, lane, 0) : p), "r"(in ? 16 : 0)
+                         : "memory");
+        } else {
+            T v[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = Elem<DT>::to_f(v.v[j]);
+            for (int j = 0; j < N; ++j) v[j] = at(slab, lane, j) < dim ? p[at(slab, lane, j)] : Elem<DT>::from_f(0.f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) reinterpret_cast<T*>(slot)[lane + 32 * j] = v[j];
+        }
+    }
+    __device__ __forceinline__ static void copies_done()
+    {
+        if (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+    }
+    __device__ __forceinline__ static void add(const uint8_t* slot, int lane, float (&acc)[N])
+    {
+        using T = typename Elem<DT>::T;
+        if (VEC) {
+            const Vec<DT> v = *reinterpret_cast<const Vec<DT>*>(slot + lane * 16);
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += Elem<DT>::to_f(v.v[VEC ? j : 0]);
         } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = at(slab, lane, j) < dim ? Elem<DT>::to_f(p[at(slab, lane, j)]) : 0.f;
+            for (int j = 0; j < N; ++j) acc[j] += Elem<DT>::to_f(reinterpret_cast<const T*>(slot)[lane + 32 * j]);
         }
     }
     // fp32 rows of `dim` values in the workspace (VEC: dim is a multiple of N, which is one of 4)
@@ -285,106 +349,127 @@ template <int DT, bool VEC> struct Columns {
     }
 };
 
-constexpr int kSumWarps = 4;
+constexpr int kSumWarps = 8;  // chunks of a block
+constexpr int kRows = 16;     // rows a warp has on their way: half a chunk of 32, a whole one of 16
+template <int DT, bool VEC> constexpr int sum_smem() { return kSumWarps * kRows * Columns<DT, VEC>::kSlotBytes; }
+
 template <int DT, int WT, bool VEC> __global__ void __launch_bounds__(32 * kSumWarps) chunk_kernel(GradArgs a)
 {
     using C = Columns<DT, VEC>;
-    const int lane = threadIdx.x & 31;
+    extern __shared__ __align__(16) uint8_t slots[];
+    __shared__ float edges[kSumWarps][2][C::N][32];  // head, tail
+    __shared__ bool starts[kSumWarps], goes_on[kSumWarps], through[kSumWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t slabs = (a.dim + C::kSlab - 1) / C::kSlab;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
-    const int64_t chunk = unit / slabs, slab = unit - chunk * slabs;
+    const int64_t block = blockIdx.x / slabs, slab = blockIdx.x - block * slabs;
+    const int64_t c0 = (block * kSumWarps + warp) * a.chunk;
+    uint8_t* mine = slots + warp * kRows * C::kSlotBytes;
     wait_for_previous();
+    allow_next();
     const int64_t n = a.start[a.vocab];
-    const int64_t c0 = chunk * a.chunk, c1 = min(n, c0 + a.chunk);
-    if (c0 >= n) return;
-    float* edge = a.edge + chunk * 2 * a.dim;
+    const int count = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(a.chunk), n - c0)));
+    // the chunk's tokens and ids, the id before it and the one after it, in one go
+    const bool has = lane < count;
+    const int32_t tok = has ? a.order[c0 + lane] : 0, key = has ? a.key[c0 + lane] : -1;
+    const int32_t prior = count > 0 && c0 > 0 ? a.key[c0 - 1] : -1, after = c0 + a.chunk < n ? a.key[c0 + a.chunk] : -1;
     float acc[C::N];
 #pragma unroll
-    for (int j = 0; j < C::N; ++j) acc[j] = 0.f;
-    int32_t now = a.key[c0];
-    bool began_before = c0 > 0 && a.key[c0 - 1] == now;
-    for (int64_t i = c0; i < c1; i += kBatch) {
-        int32_t tok = 0, key = -1;
-        if (lane <= kBatch && i + lane < n) {  // the batch's tokens, and the id after it
-            tok = a.order[i + lane];
-            key = a.key[i + lane];
-        }
-        float x[kBatch][C::N];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int64_t row = static_cast<int64_t>(__shfl_sync(0xffffffffu, tok, j)) * a.gs;
-            if (i + j < c1) C::load(a.g, row, a.dim, slab, lane, x[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int32_t next = __shfl_sync(0xffffffffu, key, j + 1);
-            if (i + j >= c1) continue;
-#pragma unroll
-            for (int k = 0; k < C::N; ++k) acc[k] += x[j][k];
-            const bool at_end = i + j + 1 == c1;
+    for (int k = 0; k < C::N; ++k) acc[k] = 0.f;
+    int32_t now = __shfl_sync(0xffffffffu, key, 0);
+    const bool began_before = count > 0 && prior == now;
+    bool first = true;
+    for (int i = 0; i < count; i += kRows) {
+        const int rows = min(kRows, count - i);
+#pragma unroll 4
+        for (int j = 0; j < rows; ++j)
+            C::fetch(mine + j * C::kSlotBytes, a.g, static_cast<int64_t>(__shfl_sync(0xffffffffu, tok, i + j)) * a.gs, a.dim, slab, lane);
+        C::copies_done();
+#pragma unroll 1
+        for (int j = 0; j < rows; ++j) {
+            const bool at_end = i + j + 1 == count;
+            const int32_t in_chunk = __shfl_sync(0xffffffffu, key, (i + j + 1) & 31);
+            const int32_t next = at_end ? after : in_chunk;
+            C::add(mine + j * C::kSlotBytes, lane, acc);
             if (next == now && !at_end) continue;
-            if (began_before) C::store_edge(edge, a.dim, slab, lane, acc);
-            else if (next == now) C::store_edge(edge + a.dim, a.dim, slab, lane, acc);
-            else C::template store<WT>(a, now, slab, lane, acc);
+            const bool head = first && began_before;
+            if (head || next == now) {
+#pragma unroll
+                for (int k = 0; k < C::N; ++k) edges[warp][head ? 0 : 1][k][lane] = acc[k];
+                if (at_end && lane == 0) through[warp] = head && next == now;
+            } else {
+                C::template store<WT>(a, now, slab, lane, acc);
+                if (at_end && lane == 0) through[warp] = false;
+            }
+            if (at_end && lane == 0) goes_on[warp] = next == now;
 #pragma unroll
             for (int k = 0; k < C::N; ++k) acc[k] = 0.f;
-            began_before = false;
+            first = false;
             now = next;
+        }
+        __syncwarp();
+    }
+    if (lane == 0) {
+        starts[warp] = began_before;
+        if (count == 0) goes_on[warp] = through[warp] = false;
+    }
+    __syncthreads();
+    // The parts of runs over the chunks' edges: the run that came into the block by warp 0,
+    // the one that begins in a warp's chunk and goes on by that warp.
+    for (int side = warp == 0 ? 0 : 1; side < 2; ++side) {
+        if (side == 0 ? !starts[0] : !(goes_on[warp] && !through[warp])) continue;
+#pragma unroll
+        for (int k = 0; k < C::N; ++k) acc[k] = edges[warp][side][k][lane];
+        bool open = side == 0 ? through[0] : true;
+        int u = warp + 1;
+        for (; open && u < kSumWarps; ++u) {
+#pragma unroll
+            for (int k = 0; k < C::N; ++k) acc[k] += edges[u][0][k][lane];
+            open = through[u];
+        }
+        if (side == 0 || open) {
+            C::store_edge(a.edge + (block * 2 + side) * a.dim, a.dim, slab, lane, acc);
+        } else {
+            C::template store<WT>(a, a.key[c0 + a.chunk - 1], slab, lane, acc);
         }
     }
 }
 
-// Runs that reach over chunks' edges: the tail where a run begins, then the heads of
-// the chunks it goes on in.  Eight warps take a stretch of them each; the stretches
-// are added in order.
-constexpr int kJoinWarps = 8;
-template <int DT, int WT, bool VEC> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(GradArgs a)
+// Runs that reach over blocks' edges: the tail where a run begins, then the heads of the
+// blocks that it goes on in.  A warp sums one run in one slab of columns.
+constexpr int kJoinWarps = 4;
+template <int DT, int WT, bool VEC> __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(GradArgs a, int64_t blocks)
 {
     using C = Columns<DT, VEC>;
-    __shared__ float sh[kJoinWarps][32][C::N + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t slabs = (a.dim + C::kSlab - 1) / C::kSlab;
-    const int64_t chunk = blockIdx.x / slabs, slab = blockIdx.x - chunk * slabs;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const int64_t slab = unit / blocks, block = unit - slab * blocks;
+    const int64_t span = static_cast<int64_t>(a.chunk) * kSumWarps, end = (block + 1) * span;
     wait_for_previous();
-    const int64_t n = a.start[a.vocab];
-    const int64_t c1 = (chunk + 1) * a.chunk;
-    if (c1 >= n) return;
-    const int32_t v = a.key[c1 - 1];
+    if (slab * C::kSlab >= a.dim || end >= a.start[a.vocab]) return;
+    const int32_t v = a.key[end - 1];
     const int64_t s0 = a.start[v], s1 = a.start[v + 1];
-    if (s1 <= c1 || s0 < c1 - a.chunk) return;  // ends here, or began before this chunk
-    const int64_t last = (s1 - 1) / a.chunk;    // the heads are those of chunks (chunk, last]
-    const int64_t parts = last - chunk + 1;
-    const int64_t per = (parts + kJoinWarps - 1) / kJoinWarps;
-    const int64_t p0 = warp * per, p1 = min(parts, p0 + per);
+    if (s1 <= end || s0 < end - span) return;  // it ends here, or began before this block
+    const int parts = static_cast<int>((s1 - 1) / span - block + 1);
+    const float* edge = a.edge + block * 2 * a.dim;
     float acc[C::N];
-#pragma unroll
-    for (int k = 0; k < C::N; ++k) acc[k] = 0.f;
-    for (int64_t p = p0; p < p1; p += 4) {
+    C::load_edge(edge + a.dim, a.dim, slab, lane, acc);
+    for (int p = 1; p < parts; p += 4) {
         float x[4][C::N];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (p + j < p1) C::load_edge(a.edge + ((chunk + p + j) * 2 + (p + j == 0)) * a.dim, a.dim, slab, lane, x[j]);
+            if (p + j < parts) C::load_edge(edge + (p + j) * 2 * a.dim, a.dim, slab, lane, x[j]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (p + j < p1)
+            if (p + j < parts)
 #pragma unroll
                 for (int k = 0; k < C::N; ++k) acc[k] += x[j][k];
     }
-#pragma unroll
-    for (int k = 0; k < C::N; ++k) sh[warp][lane][k] = acc[k];
-    __syncthreads();
-    if (warp == 0) {
-        const int used = static_cast<int>(min(static_cast<int64_t>(kJoinWarps), (parts + per - 1) / per));
-        for (int w = 1; w < used; ++w)
-#pragma unroll
-            for (int k = 0; k < C::N; ++k) acc[k] += sh[w][lane][k];
-        C::template store<WT>(a, v, slab, lane, acc);
-    }
+    C::template store<WT>(a, v, slab, lane, acc);
 }
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Tokens a warp sums: short chunks spread few tokens over the SMs, longer ones write fewer edges.
+// Tokens a warp sums: short chunks spread few tokens over the SMs, longer ones have fewer edges.
 int32_t chunk_for(int64_t ntokens) { return ntokens <= 16384 ? 16 : 32; }
 
 struct EmbeddingSpace {
@@ -398,7 +483,8 @@ EmbeddingSpace space_for(int64_t ntokens, int64_t vocab, int64_t dim)
     e.key = e.order + round_up(4 * ntokens, 256);
     e.start = e.key + round_up(4 * ntokens, 256);
     e.edge = e.start + round_up(4 * (vocab + 1), 256);
-    e.total = e.edge + round_up((ntokens + chunk - 1) / chunk * 8 * dim, 256);
+    const int64_t span = chunk * kSumWarps;
+    e.total = e.edge + round_up((ntokens + span - 1) / span * 8 * dim, 256);
     return e;
 }
 
@@ -432,11 +518,20 @@ template <int DT> void launch_lookup(bool vec, int grid, cudaStream_t s, const v
 template <int DT, int WT, bool VEC> cudaError_t launch_sums_as(const GradArgs& g, int64_t ntokens, cudaStream_t s)
 {
     const int64_t slabs = (g.dim + Columns<DT, VEC>::kSlab - 1) / Columns<DT, VEC>::kSlab;
-    const int64_t units = (ntokens + g.chunk - 1) / g.chunk * slabs;
-    const cudaError_t e = launch_chained(chunk_kernel<DT, WT, VEC>, dim3(static_cast<unsigned>((units + kSumWarps - 1) / kSumWarps)),
-                                         32 * kSumWarps, 0, s, g);
-    if (e != cudaSuccess) return e;
-    return launch_chained(join_kernel<DT, WT, VEC>, dim3(static_cast<unsigned>(units)), 32 * kJoinWarps, 0, s, g);
+    const int64_t span = static_cast<int64_t>(g.chunk) * kSumWarps, blocks = (ntokens + span - 1) / span;
+    constexpr int smem = sum_smem<DT, VEC>();
+    static std::atomic<bool> ready[ddp::kMaxDevices] = {};
+    const int dev = ddp::current_device();
+    cudaError_t e;
+    if (dev < 0 || !ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(chunk_kernel<DT, WT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0) ready[dev].store(true, std::memory_order_relaxed);
+    }
+    e = launch_chained(chunk_kernel<DT, WT, VEC>, dim3(static_cast<unsigned>(blocks * slabs)), 32 * kSumWarps, smem, s, g);
+    if (e != cudaSuccess || blocks == 1) return e;
+    return launch_chained(join_kernel<DT, WT, VEC>, dim3(static_cast<unsigned>((blocks * slabs + kJoinWarps - 1) / kJoinWarps)),
+                          32 * kJoinWarps, 0, s, g, blocks);
 }
 template <int DT> cudaError_t launch_sums(const GradArgs& g, int64_t ntokens, int gw_dtype, bool vec, cudaStream_t s)
 {
@@ -536,12 +631,14 @@ extern "C" ddp_status ddp_embedding_backward(const void* grad_out, int64_t grad_
     const int dev = ddp::current_device();
     cudaError_t err = cudaSuccess;
     if (dev < 0 || !ready[dev].load(std::memory_order_relaxed)) {
-        err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortWarps * kMaxRange * 4);
+        err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
         if (err != cudaSuccess) return fail(DDP_E_CUDA, "%s: shared memory: %s", fn, cudaGetErrorString(err));
         if (dev >= 0) ready[dev].store(true, std::memory_order_relaxed);
     }
+    const int64_t counters = kSortWarps * a.range * 4;
+    a.cached = counters + 2 * ntokens <= kSortSmem;
     err = launch_chained(sort_kernel, dim3(static_cast<unsigned>((vocab + a.range - 1) / a.range)), kSortThreads,
-                         kSortWarps * a.range * 4, s, a);
+                         static_cast<int>(counters + (a.cached ? 2 * ntokens : 0)), s, a);
     if (err == cudaSuccess && ntokens > 0) {
         const GradArgs g{grad_out, grad_stride, a.order, a.key, a.start, vocab, dim, chunk_for(ntokens),
                          reinterpret_cast<float*>(w + sp.edge), scale, grad_weight, gw_stride, accumulate != 0};
