@@ -6,10 +6,13 @@
 // order) and each row of dW is the fp32 sum of its run, taken in that order: no
 // atomics, the same bits every time.  HBM-bound: dY is read once, dW written once.
 //
-// Sort: one launch in which every CTA owns a range of ids, reads all the tokens
-// and keeps those of its range.  A token's place is (tokens with smaller ids) +
-// (earlier tokens with its id); the first count covers the ranges before the CTA's
-// too, so no CTA needs a result of another.
+// Sort: one launch in which each of N CTAs owns the ids that leave its number as the
+// remainder by N, reads all the tokens and keeps those of its ids.  A token's place is
+// (tokens with smaller remainders) + (tokens with its remainder and smaller ids) +
+// (earlier tokens with its id): no CTA needs a result of another.  The order that comes
+// out keeps equal ids together, which is all the sums need, and the frequent ids, which
+// are often neighbours, are dealt out over the CTAs (with ranges of neighbouring ids the
+// owner of the most frequent ones took 84 us where even ids took 31, at 65521 tokens).
 #include <algorithm>
 #include <atomic>
 
@@ -76,6 +79,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr uint16_t kNone = 0xffff;
 constexpr int kMaxRange = 1024;  // ids a sorting CTA owns at most (its counters: 4 bytes an id and warp)
+constexpr int kMinSortCtas = 128;  // a power of two, one wave
 constexpr int kIdBatch = 8;      // loads of ids a thread keeps in flight
 constexpr int kSortSmem = 220 * 1024;  // counters, and the tokens' places in the range where they fit
 
@@ -84,10 +88,12 @@ struct SortArgs {
     int32_t id_bytes;
     int32_t ntokens;
     int64_t vocab, padding_idx;
-    int32_t range;   // ids per CTA
-    int32_t* order;  // [ntokens] tokens sorted by id
+    int32_t range;   // ids per CTA at most
+    int32_t shift;   // 2^shift CTAs
+    int32_t* order;  // [ntokens] sorted tokens
     int32_t* key;    // [ntokens] their ids
-    int32_t* start;  // [vocab + 1] first place of each id in `order`
+    int2* run;       // [vocab] first place of each id in `order` and the one after its last
+    int32_t* total;  // tokens in `order`
     int* status;
     int32_t cached;  // the second pass reads what the first one left in shared memory
     // rows of ids that do not occur (nullptr: left alone)
@@ -103,36 +109,33 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t* cnt = sh + warp * a.range;
     uint16_t* place = reinterpret_cast<uint16_t*>(sh + kSortWarps * a.range);  // [ntokens], where it fits
-    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.range;
-    const int64_t hi = lo + a.range < a.vocab ? lo + a.range : a.vocab;
-    const int nr = static_cast<int>(hi - lo);
+    // the CTA's ids: own + (r << shift), r < nr
+    const uint32_t own = blockIdx.x, mask = (1u << a.shift) - 1u, vocab32 = static_cast<uint32_t>(a.vocab);
+    const uint32_t pad32 = a.padding_idx >= 0 && a.padding_idx < a.vocab ? static_cast<uint32_t>(a.padding_idx) : 0xffffffffu;
+    const int nr = own < vocab32 ? static_cast<int>((vocab32 - own - 1) >> a.shift) + 1 : 0;
     for (int i = tid; i < kSortWarps * a.range; i += kSortThreads) sh[i] = 0;
     __syncthreads();
     wait_for_previous();
-    // An id relative to the range, as far as it is one of the range's; kNone: another's.
-    // (ids of 2^31 and more are out of any vocabulary)
-    const uint32_t lo32 = static_cast<uint32_t>(lo), vocab32 = static_cast<uint32_t>(a.vocab);
-    const uint32_t pad32 = a.padding_idx >= 0 && a.padding_idx < a.vocab ? static_cast<uint32_t>(a.padding_idx) : 0xffffffffu;
-    auto in_range = [&](int64_t id) {
-        const uint32_t x = static_cast<uint32_t>(id);
-        const bool good = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32 && x != pad32;
-        return good && x - lo32 < static_cast<uint32_t>(nr) ? static_cast<uint16_t>(x - lo32) : kNone;
-    };
     // each warp counts a contiguous stretch of tokens (a multiple of 64 of them)
     const int per = (a.ntokens + 64 * kSortWarps - 1) / (64 * kSortWarps) * 64;
     const int t0 = min(warp * per, a.ntokens), t1 = min(t0 + per, a.ntokens);
     int32_t less = 0;
     bool bad = false;
-    auto count = [&](int t, int64_t id) {
+    // which of the CTA's ids a token has (kNone: none of them); ids of 2^31 and more are out of any vocabulary
+    auto row_of = [&](int64_t id, bool* known, bool* before) {
         const uint32_t x = static_cast<uint32_t>(id);
-        const bool known = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32;
+        *known = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32;
+        const bool counts = *known && x != pad32;
+        *before = counts && (x & mask) < own;
+        return counts && (x & mask) == own ? static_cast<uint16_t>(x >> a.shift) : kNone;
+    };
+    auto count = [&](int64_t id) {
+        bool known, before;
+        const uint16_t r = row_of(id, &known, &before);
         bad |= !known;
-        const uint32_t r = x - lo32;
-        const bool counts = known && x != pad32;
-        less += counts && x < lo32;
-        const bool mine = counts && r < static_cast<uint32_t>(nr);
-        if (mine) atomicAdd(&cnt[r], 1);
-        if (a.cached) place[t] = mine ? static_cast<uint16_t>(r) : kNone;
+        less += before;
+        if (r != kNone) atomicAdd(&cnt[r], 1);
+        return r;
     };
     // pairs of ids in 16-byte (8-byte) loads where the list starts on such a boundary
     const bool pairs = (reinterpret_cast<uintptr_t>(a.ids) & (2 * a.id_bytes - 1)) == 0;
@@ -154,11 +157,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
 #pragma unroll
         for (int j = 0; j < kIdBatch; ++j) {
             if (t + 64 * j >= whole) continue;
-            count(t + 64 * j, id[j][0]);
-            count(t + 64 * j + 1, id[j][1]);
+            const uint32_t p = count(id[j][0]), q = count(id[j][1]);
+            if (a.cached) *reinterpret_cast<uint32_t*>(place + t + 64 * j) = p | (q << 16);  // t is even
         }
     }
-    for (int t = whole + lane; t < t1; t += 32) count(t, load_id(a.ids, a.id_bytes, t));
+    for (int t = whole + lane; t < t1; t += 32) {
+        const uint16_t p = count(load_id(a.ids, a.id_bytes, t));
+        if (a.cached) place[t] = p;
+    }
     if (bad && blockIdx.x == 0) atomicOr(a.status, kErrId);
 #pragma unroll
     for (int o = 16; o; o >>= 1) less += __shfl_xor_sync(0xffffffffu, less, o);
@@ -180,11 +186,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
     __syncthreads();
     int32_t before = base;
     for (int w = 0; w < warp; ++w) before += part[w];
+    // the last CTA's tokens are the last
+    if (blockIdx.x + 1 == gridDim.x && tid == kSortThreads - 1) *a.total = before + inc;
     if (tid < nr) {
         int32_t at = before + inc - total;
         seen[tid] = total > 0;
-        a.start[lo + tid] = at;
-        if (lo + tid + 1 == a.vocab) a.start[a.vocab] = at + total;
+        a.run[own + (static_cast<uint32_t>(tid) << a.shift)] = make_int2(at, at + total);
         // the counters become the first places of the id's tokens from each warp's stretch
         for (int w = 0; w < kSortWarps; ++w) {
             const int32_t c = sh[w * a.range + tid];
@@ -193,35 +200,50 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
         }
     }
     __syncthreads();
-    for (int t = t0; t < t1; t += 32 * kIdBatch) {
-        uint16_t at_row[kIdBatch];
+    // 64 tokens at a time, two a lane: most groups have none of the CTA's ids
+    for (int t = t0; t < t1; t += 64 * kIdBatch) {
+        uint32_t rows[kIdBatch];
 #pragma unroll
         for (int j = 0; j < kIdBatch; ++j) {
-            const int u = t + 32 * j + lane;
-            at_row[j] = u >= t1 ? kNone : a.cached ? place[u] : in_range(load_id(a.ids, a.id_bytes, u));
+            const int u = t + 64 * j + 2 * lane;
+            rows[j] = 0xffffffffu;
+            if (u >= t1) continue;
+            if (a.cached) {
+                rows[j] = *reinterpret_cast<const uint32_t*>(place + u);
+                if (u + 1 >= t1) rows[j] |= 0xffff0000u;
+            } else {
+                bool k, l;
+                const uint32_t p = row_of(load_id(a.ids, a.id_bytes, u), &k, &l);
+                const uint32_t q = u + 1 < t1 ? row_of(load_id(a.ids, a.id_bytes, u + 1), &k, &l) : kNone;
+                rows[j] = p | (q << 16);
+            }
         }
 #pragma unroll
         for (int j = 0; j < kIdBatch; ++j) {
-            const bool mine = at_row[j] != kNone;
-            const uint32_t any = __ballot_sync(0xffffffffu, mine);
-            if (!any) continue;
-            if (mine) {
-                const int r = at_row[j];
-                const uint32_t same = __match_any_sync(any, r);
-                const int at = cnt[r] + __popc(same & ((1u << lane) - 1u));
-                a.order[at] = t + 32 * j + lane;
-                a.key[at] = static_cast<int32_t>(lo32 + r);
-                __syncwarp(same);
-                if (lane == __ffs(same) - 1) cnt[r] += __popc(same);
+            if (!__any_sync(0xffffffffu, rows[j] != 0xffffffffu)) continue;
+            // the first 32 tokens of the group, then the others: lane i takes token i of the half
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t pair = __shfl_sync(0xffffffffu, rows[j], half * 16 + (lane >> 1));
+                const int r = static_cast<int>((lane & 1) ? pair >> 16 : pair & 0xffffu);
+                const bool mine = r != kNone;
+                const uint32_t any = __ballot_sync(0xffffffffu, mine);
+                if (mine) {
+                    const uint32_t same = __match_any_sync(any, r);
+                    const int at = cnt[r] + __popc(same & ((1u << lane) - 1u));
+                    a.order[at] = t + 64 * j + 32 * half + lane;
+                    a.key[at] = static_cast<int32_t>(own + (static_cast<uint32_t>(r) << a.shift));
+                    __syncwarp(same);
+                    if (lane == __ffs(same) - 1) cnt[r] += __popc(same);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
-    // the rest of the range's rows: nothing to wait for
+    // the rows of the CTA's ids that do not occur: nothing to wait for
     if (a.clear) {
         for (int r = warp; r < nr; r += kSortWarps) {
             if (seen[r]) continue;
-            uint8_t* row = a.clear + (lo + r) * a.clear_stride;
+            uint8_t* row = a.clear + (own + (static_cast<int64_t>(r) << a.shift)) * a.clear_stride;
             const int64_t head = min(a.clear_bytes, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15));
             const int64_t body = head + (a.clear_bytes - head) / 16 * 16;
             if (lane * 2 < head) *reinterpret_cast<uint16_t*>(row + lane * 2) = 0;
@@ -243,8 +265,9 @@ struct GradArgs {
     int64_t gs;
     const int32_t* order;
     const int32_t* key;
-    const int32_t* start;
-    int64_t vocab, dim;
+    const int2* run;
+    const int32_t* total;
+    int64_t ntokens, dim;
     int32_t chunk;
     float* edge;  // [blocks][head, tail][dim]
     float scale;
@@ -262,7 +285,7 @@ template <int DT, bool VEC> struct Columns {
         return slab * kSlab + (VEC ? lane * N + j : lane + 32 * j);
     }
     // A row's columns into a warp's slot of kSlotBytes; past the row's end, zeros.  VEC: an
-    // asynchronous copy, complete after copies_done().
+    // asynchronous copy, complete after batch_done().
     static constexpr int kSlotBytes = 32 * N * static_cast<int>(sizeof(typename Elem<DT>::T));
     __device__ __forceinline__ static void fetch(uint8_t* slot, const void* g, int64_t row, int64_t dim, int64_t slab, int lane)
     {
@@ -282,9 +305,14 @@ template <int DT, bool VEC> struct Columns {
             for (int j = 0; j < N; ++j) reinterpret_cast<T*>(slot)[lane + 32 * j] = v[j];
         }
     }
-    __device__ __forceinline__ static void copies_done()
+    __device__ __forceinline__ static void batch_end()
     {
-        if (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (VEC) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // all batches but the newest are there
+    __device__ __forceinline__ static void batch_done()
+    {
+        if (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
     }
     __device__ __forceinline__ static void add(const uint8_t* slot, int lane, float (&acc)[N])
@@ -350,8 +378,8 @@ template <int DT, bool VEC> struct Columns {
 };
 
 constexpr int kSumWarps = 8;  // chunks of a block
-constexpr int kRows = 16;     // rows a warp has on their way: half a chunk of 32, a whole one of 16
-template <int DT, bool VEC> constexpr int sum_smem() { return kSumWarps * kRows * Columns<DT, VEC>::kSlotBytes; }
+constexpr int kRows = 8;      // rows of a batch; a warp has two on their way
+template <int DT, bool VEC> constexpr int sum_smem() { return kSumWarps * 2 * kRows * Columns<DT, VEC>::kSlotBytes; }
 
 template <int DT, int WT, bool VEC> __global__ void __launch_bounds__(32 * kSumWarps) chunk_kernel(GradArgs a)
 {
@@ -363,33 +391,45 @@ template <int DT, int WT, bool VEC> __global__ void __launch_bounds__(32 * kSumW
     const int64_t slabs = (a.dim + C::kSlab - 1) / C::kSlab;
     const int64_t block = blockIdx.x / slabs, slab = blockIdx.x - block * slabs;
     const int64_t c0 = (block * kSumWarps + warp) * a.chunk;
-    uint8_t* mine = slots + warp * kRows * C::kSlotBytes;
+    uint8_t* mine = slots + warp * 2 * kRows * C::kSlotBytes;
     wait_for_previous();
     allow_next();
-    const int64_t n = a.start[a.vocab];
+    // the chunk's tokens and ids, the id before it and the one after it, and how many tokens
+    // there are, in one go (what lies past the last token is left over from before)
+    const bool in = lane < a.chunk && c0 + lane < a.ntokens;
+    int32_t tok = in ? a.order[c0 + lane] : 0, key = in ? a.key[c0 + lane] : -1;
+    int32_t prior = c0 > 0 && c0 < a.ntokens ? a.key[c0 - 1] : -1, after = c0 + a.chunk < a.ntokens ? a.key[c0 + a.chunk] : -1;
+    const int64_t n = *a.total;
     const int count = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(a.chunk), n - c0)));
-    // the chunk's tokens and ids, the id before it and the one after it, in one go
-    const bool has = lane < count;
-    const int32_t tok = has ? a.order[c0 + lane] : 0, key = has ? a.key[c0 + lane] : -1;
-    const int32_t prior = count > 0 && c0 > 0 ? a.key[c0 - 1] : -1, after = c0 + a.chunk < n ? a.key[c0 + a.chunk] : -1;
+    if (lane >= count) tok = 0, key = -1;
+    if (c0 + a.chunk >= n) after = -1;
     float acc[C::N];
 #pragma unroll
     for (int k = 0; k < C::N; ++k) acc[k] = 0.f;
     int32_t now = __shfl_sync(0xffffffffu, key, 0);
     const bool began_before = count > 0 && prior == now;
     bool first = true;
-    for (int i = 0; i < count; i += kRows) {
+    // two buffers of kRows rows: one is on its way while the other is summed
+    auto fetch = [&](int i) {
+        uint8_t* to = mine + (i / kRows & 1) * kRows * C::kSlotBytes;
         const int rows = min(kRows, count - i);
 #pragma unroll 4
         for (int j = 0; j < rows; ++j)
-            C::fetch(mine + j * C::kSlotBytes, a.g, static_cast<int64_t>(__shfl_sync(0xffffffffu, tok, i + j)) * a.gs, a.dim, slab, lane);
-        C::copies_done();
+            C::fetch(to + j * C::kSlotBytes, a.g, static_cast<int64_t>(__shfl_sync(0xffffffffu, tok, i + j)) * a.gs, a.dim, slab, lane);
+        C::batch_end();
+    };
+    fetch(0);
+    for (int i = 0; i < count; i += kRows) {
+        const int rows = min(kRows, count - i);
+        const uint8_t* from = mine + (i / kRows & 1) * kRows * C::kSlotBytes;
+        fetch(i + kRows);
+        C::batch_done();
 #pragma unroll 1
         for (int j = 0; j < rows; ++j) {
             const bool at_end = i + j + 1 == count;
             const int32_t in_chunk = __shfl_sync(0xffffffffu, key, (i + j + 1) & 31);
             const int32_t next = at_end ? after : in_chunk;
-            C::add(mine + j * C::kSlotBytes, lane, acc);
+            C::add(from + j * C::kSlotBytes, lane, acc);
             if (next == now && !at_end) continue;
             const bool head = first && began_before;
             if (head || next == now) {
@@ -445,9 +485,9 @@ template <int DT, int WT, bool VEC> __global__ void __launch_bounds__(32 * kJoin
     const int64_t slab = unit / blocks, block = unit - slab * blocks;
     const int64_t span = static_cast<int64_t>(a.chunk) * kSumWarps, end = (block + 1) * span;
     wait_for_previous();
-    if (slab * C::kSlab >= a.dim || end >= a.start[a.vocab]) return;
+    if (slab * C::kSlab >= a.dim || end >= *a.total) return;
     const int32_t v = a.key[end - 1];
-    const int64_t s0 = a.start[v], s1 = a.start[v + 1];
+    const int64_t s0 = a.run[v].x, s1 = a.run[v].y;
     if (s1 <= end || s0 < end - span) return;  // it ends here, or began before this block
     const int parts = static_cast<int>((s1 - 1) / span - block + 1);
     const float* edge = a.edge + block * 2 * a.dim;
@@ -473,7 +513,7 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int32_t chunk_for(int64_t ntokens) { return ntokens <= 16384 ? 16 : 32; }
 
 struct EmbeddingSpace {
-    int64_t order, key, start, edge, total;  // byte offsets
+    int64_t order, key, run, count, edge, total;  // byte offsets
 };
 EmbeddingSpace space_for(int64_t ntokens, int64_t vocab, int64_t dim)
 {
@@ -481,8 +521,9 @@ EmbeddingSpace space_for(int64_t ntokens, int64_t vocab, int64_t dim)
     const int64_t chunk = chunk_for(ntokens);
     e.order = 0;
     e.key = e.order + round_up(4 * ntokens, 256);
-    e.start = e.key + round_up(4 * ntokens, 256);
-    e.edge = e.start + round_up(4 * (vocab + 1), 256);
+    e.run = e.key + round_up(4 * ntokens, 256);
+    e.count = e.run + round_up(8 * vocab, 256);
+    e.edge = e.count + 256;
     const int64_t span = chunk * kSumWarps;
     e.total = e.edge + round_up((ntokens + span - 1) / span * 8 * dim, 256);
     return e;
@@ -618,15 +659,18 @@ extern "C" ddp_status ddp_embedding_backward(const void* grad_out, int64_t grad_
     a.padding_idx = padding_idx;
     a.order = reinterpret_cast<int32_t*>(w + sp.order);
     a.key = reinterpret_cast<int32_t*>(w + sp.key);
-    a.start = reinterpret_cast<int32_t*>(w + sp.start);
+    a.run = reinterpret_cast<int2*>(w + sp.run);
+    a.total = reinterpret_cast<int32_t*>(w + sp.count);
     a.status = status;
     if (!accumulate) {
         a.clear = static_cast<uint8_t*>(grad_weight);
         a.clear_stride = gw_stride * es;
         a.clear_bytes = dim * es;
     }
-    const int sms = ddp::device_sm_count();
-    a.range = static_cast<int32_t>(std::min<int64_t>(kMaxRange, std::max<int64_t>(1, (vocab + sms - 1) / sms)));
+    int64_t ctas = kMinSortCtas;
+    while ((vocab + ctas - 1) / ctas > kMaxRange) ctas *= 2;
+    while ((int64_t{1} << a.shift) < ctas) ++a.shift;
+    a.range = static_cast<int32_t>((vocab + ctas - 1) / ctas);
     static std::atomic<bool> ready[ddp::kMaxDevices] = {};
     const int dev = ddp::current_device();
     cudaError_t err = cudaSuccess;
@@ -636,11 +680,11 @@ extern "C" ddp_status ddp_embedding_backward(const void* grad_out, int64_t grad_
         if (dev >= 0) ready[dev].store(true, std::memory_order_relaxed);
     }
     const int64_t counters = kSortWarps * a.range * 4;
-    a.cached = counters + 2 * ntokens <= kSortSmem;
-    err = launch_chained(sort_kernel, dim3(static_cast<unsigned>((vocab + a.range - 1) / a.range)), kSortThreads,
-                         static_cast<int>(counters + (a.cached ? 2 * ntokens : 0)), s, a);
+    a.cached = counters + 2 * ntokens + 4 <= kSortSmem;
+    err = launch_chained(sort_kernel, dim3(static_cast<unsigned>(ctas)), kSortThreads,
+                         static_cast<int>(counters + (a.cached ? 2 * ntokens + 4 : 0)), s, a);
     if (err == cudaSuccess && ntokens > 0) {
-        const GradArgs g{grad_out, grad_stride, a.order, a.key, a.start, vocab, dim, chunk_for(ntokens),
+        const GradArgs g{grad_out, grad_stride, a.order, a.key, a.run, a.total, ntokens, dim, chunk_for(ntokens),
                          reinterpret_cast<float*>(w + sp.edge), scale, grad_weight, gw_stride, accumulate != 0};
         const int n = 16 / elem_size(dtype);
         const bool vec = dim % n == 0 && grad_stride % n == 0 && gw_stride % n == 0 && aligned16(grad_out) && aligned16(grad_weight);
