@@ -121,22 +121,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
     const int t0 = min(warp * per, a.ntokens), t1 = min(t0 + per, a.ntokens);
     int32_t less = 0;
     bool bad = false;
-    // which of the CTA's ids a token has (kNone: none of them); ids of 2^31 and more are out of any vocabulary
-    auto row_of = [&](int64_t id, bool* known, bool* before) {
+    // The remainder of a token's id, or one that no CTA has; ids of 2^31 and more are out of
+    // any vocabulary.  (Few instructions: every CTA looks at every token.)
+    auto remainder = [&](int64_t id) {
         const uint32_t x = static_cast<uint32_t>(id);
-        *known = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32;
-        const bool counts = *known && x != pad32;
-        *before = counts && (x & mask) < own;
-        return counts && (x & mask) == own ? static_cast<uint16_t>(x >> a.shift) : kNone;
+        const bool known = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) == 0 && x < vocab32;
+        if (blockIdx.x == 0) bad |= !known;
+        return known && x != pad32 ? x & mask : 0xffffffffu;
     };
-    auto count = [&](int64_t id) {
-        bool known, before;
-        const uint16_t r = row_of(id, &known, &before);
-        bad |= !known;
-        less += before;
-        if (r != kNone) atomicAdd(&cnt[r], 1);
-        return r;
-    };
+    auto row_of = [&](uint32_t rem, int64_t id) { return rem == own ? static_cast<uint32_t>(id) >> a.shift : uint32_t{kNone}; };
     // pairs of ids in 16-byte (8-byte) loads where the list starts on such a boundary
     const bool pairs = (reinterpret_cast<uintptr_t>(a.ids) & (2 * a.id_bytes - 1)) == 0;
     const int whole = pairs ? t0 + (t1 - t0) / 2 * 2 : t0;
@@ -157,15 +150,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
 #pragma unroll
         for (int j = 0; j < kIdBatch; ++j) {
             if (t + 64 * j >= whole) continue;
-            const uint32_t p = count(id[j][0]), q = count(id[j][1]);
-            if (a.cached) *reinterpret_cast<uint32_t*>(place + t + 64 * j) = p | (q << 16);  // t is even
+            const uint32_t p = remainder(id[j][0]), q = remainder(id[j][1]);
+            less += (p < own) + (q < own);
+            uint32_t rows = 0xffffffffu;
+            if (p == own || q == own) {
+                rows = row_of(p, id[j][0]) | (row_of(q, id[j][1]) << 16);
+                if (p == own) atomicAdd(&cnt[rows & 0xffffu], 1);
+                if (q == own) atomicAdd(&cnt[rows >> 16], 1);
+            }
+            if (a.cached) *reinterpret_cast<uint32_t*>(place + t + 64 * j) = rows;  // t is even
         }
     }
     for (int t = whole + lane; t < t1; t += 32) {
-        const uint16_t p = count(load_id(a.ids, a.id_bytes, t));
-        if (a.cached) place[t] = p;
+        const int64_t id = load_id(a.ids, a.id_bytes, t);
+        const uint32_t p = remainder(id), r = row_of(p, id);
+        less += p < own;
+        if (r != kNone) atomicAdd(&cnt[r], 1);
+        if (a.cached) place[t] = static_cast<uint16_t>(r);
     }
-    if (bad && blockIdx.x == 0) atomicOr(a.status, kErrId);
+    if (bad) atomicOr(a.status, kErrId);
 #pragma unroll
     for (int o = 16; o; o >>= 1) less += __shfl_xor_sync(0xffffffffu, less, o);
     if (lane == 0) less_w[warp] = less;
@@ -212,10 +215,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a)
                 rows[j] = *reinterpret_cast<const uint32_t*>(place + u);
                 if (u + 1 >= t1) rows[j] |= 0xffff0000u;
             } else {
-                bool k, l;
-                const uint32_t p = row_of(load_id(a.ids, a.id_bytes, u), &k, &l);
-                const uint32_t q = u + 1 < t1 ? row_of(load_id(a.ids, a.id_bytes, u + 1), &k, &l) : kNone;
-                rows[j] = p | (q << 16);
+                const int64_t p = load_id(a.ids, a.id_bytes, u), q = u + 1 < t1 ? load_id(a.ids, a.id_bytes, u + 1) : -1;
+                rows[j] = row_of(remainder(p), p) | (row_of(remainder(q), q) << 16);
             }
         }
 #pragma unroll
@@ -537,7 +538,7 @@ ddp_status check_common(const char* fn, int64_t ntokens, int64_t vocab, int64_t 
     if (ntokens >= (int64_t{1} << 31)) return fail(DDP_E_INVAL, "%s: ntokens = %lld is 2^31 or more", fn, static_cast<long long>(ntokens));
     if (vocab < 1 || vocab >= (int64_t{1} << 31))
         return fail(DDP_E_INVAL, "%s: vocab = %lld outside [1, 2^31)", fn, static_cast<long long>(vocab));
-    if (dim < 1) return fail(DDP_E_INVAL, "%s: dim = %lld < 1", fn, static_cast<long long>(dim));
+    if (dim < 1 || dim >= (int64_t{1} << 28)) return fail(DDP_E_INVAL, "%s: dim = %lld outside [1, 2^28)", fn, static_cast<long long>(dim));
     if (!known_dtype(dtype)) return fail(DDP_E_INVAL, "%s: unknown dtype %d", fn, dtype);
     if (id_bytes != 4 && id_bytes != 8) return fail(DDP_E_INVAL, "%s: id_bytes = %d is neither 4 nor 8", fn, id_bytes);
     if (mat_stride < dim)
@@ -619,7 +620,7 @@ extern "C" ddp_status ddp_embedding_workspace(int64_t ntokens, int64_t vocab, in
 {
     const char* fn = "ddp_embedding_workspace";
     if (!bytes) return ddp::fail(DDP_E_INVAL, "%s: bytes is NULL", fn);
-    if (ntokens < 0 || ntokens >= (int64_t{1} << 31) || vocab < 1 || vocab >= (int64_t{1} << 31) || dim < 1)
+    if (ntokens < 0 || ntokens >= (int64_t{1} << 31) || vocab < 1 || vocab >= (int64_t{1} << 31) || dim < 1 || dim >= (int64_t{1} << 28))
         return ddp::fail(DDP_E_INVAL, "%s: ntokens = %lld, vocab = %lld, dim = %lld out of range", fn,
                          static_cast<long long>(ntokens), static_cast<long long>(vocab), static_cast<long long>(dim));
     *bytes = space_for(ntokens, vocab, dim).total;

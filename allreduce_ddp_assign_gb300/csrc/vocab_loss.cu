@@ -24,6 +24,8 @@ namespace {
 
 constexpr int kRowTile = 256;   // rows of the gathered arrays are padded to this
 constexpr int kPrepThreads = 256;
+constexpr int kFewTokens = 2;      // up to so many the forward pass goes without matrix products
+constexpr int kMaxFewCtas = 1024;
 // elements of G that are held at a time: 268 MB
 constexpr int64_t kPieceElements = int64_t{1} << 27;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,7 +84,8 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
         const int64_t nt = (D + 255) / 256;
         s.acc = take(4 * s.dpad * (s.tpad + kRowTile * ((kSplitTiles + nt - 1) / nt)));
     } else {
-        s.part = take(8 * s.tpad * s.ntiles);
+        // (for a few tokens: a pair for each token and CTA)
+        s.part = take(std::max<int64_t>(8 * s.tpad * s.ntiles, 8 * kFewTokens * kMaxFewCtas));
         s.ztarget = take(4 * s.tpad);
     }
     if (copy_weight) s.weight = take(2 * V * s.dpad);
@@ -933,8 +936,8 @@ __device__ __forceinline__ float2 join_pairs(float2 a, float2 b)
 {
     const float m = fmaxf(a.x, b.x);
     // a side whose words are all minus infinity brings 0 (or a NaN, which stays)
-    const float sa = a.x == -INFINITY ? a.y : a.y * exp2f((a.x - m) * kLog2e);
-    const float sb = b.x == -INFINITY ? b.y : b.y * exp2f((b.x - m) * kLog2e);
+    const float sa = a.x == -INFINITY ? a.y : a.y * pow2((a.x - m) * kLog2e);
+    const float sb = b.x == -INFINITY ? b.y : b.y * pow2((b.x - m) * kLog2e);
     return make_float2(m, sa + sb);
 }
 // The target's logit is computed again with fp32 multiply-adds: the tensor cores cut
@@ -991,6 +994,158 @@ combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, in
     }
 }
 
+// ---------------------------------------------------------------------------
+// forward for a few tokens
+// ---------------------------------------------------------------------------
+// HBM-bound: the weight is read once, a warp takes four of its rows at a time and
+// multiplies them with every token's hidden state, which shared memory holds.  At 50257 x
+// 768 one token takes 29 us (50 on the tensor cores), two take 38 (50), four 66 (52).
+constexpr int kFewElements = 32768;  // of hidden states in shared memory
+constexpr int kFewThreads = 256;
+constexpr int kFewRows = 4;  // (the reduction over the lanes is written for four)
+constexpr int kFewPerSm = 3;
+
+struct FewArgs {
+    const void* hidden;
+    int64_t hs;
+    const void* weight;
+    int64_t ws, V, D;
+    const void* targets;
+    int32_t id_bytes, T;
+    int64_t ignore;
+    float2* part;   // [token][CTA]
+    float* ztarget;
+    float* loss;
+    float* lse;
+    int32_t ctas;
+    int* status;
+};
+
+template <int DT, int NT, bool VEC> __global__ void __launch_bounds__(kFewThreads, kFewPerSm) few_kernel(FewArgs a)
+{
+    using T = typename Elem<DT>::T;
+    extern __shared__ __align__(16) uint8_t few_smem[];
+    __shared__ float2 joined[kFewThreads / 32][NT];
+    T* h = reinterpret_cast<T*>(few_smem);  // [NT][dpad], zeros past the row's end
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t dpad = (a.D + 7) / 8 * 8;
+    wait_for_previous();
+    int64_t y[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) y[t] = t < a.T ? load_id(a.targets, a.id_bytes, t) : a.ignore;
+    for (int64_t i = tid; i < NT * dpad; i += kFewThreads) {
+        const int64_t t = i / dpad, c = i - t * dpad;
+        h[i] = t < a.T && c < a.D ? static_cast<const T*>(a.hidden)[t * a.hs + c] : Elem<DT>::from_f(0.f);
+    }
+    __syncthreads();
+    float2 st[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) st[t] = make_float2(-INFINITY, 0.f);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
+    for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp) * kFewRows; v0 < a.V; v0 += warps * kFewRows) {
+        float z[kFewRows][NT] = {};
+        // rows past the last word read the last word's
+        const T* w[kFewRows];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) w[r] = static_cast<const T*>(a.weight) + min(v0 + r, a.V - 1) * a.ws;
+        if (VEC) {
+            const int64_t whole = a.D / 8 * 8;
+#pragma unroll 3
+            for (int64_t c = lane * 8; c < whole; c += 256) {
+                Vec<DT> x[kFewRows];
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r) x[r] = *reinterpret_cast<const Vec<DT>*>(w[r] + c);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const Vec<DT> q = *reinterpret_cast<const Vec<DT>*>(h + t * dpad + c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int r = 0; r < kFewRows; ++r) z[r][t] = fmaf(Elem<DT>::to_f(x[r].v[j]), Elem<DT>::to_f(q.v[j]), z[r][t]);
+                }
+            }
+            if (whole + lane < a.D) {
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        z[r][t] = fmaf(Elem<DT>::to_f(w[r][whole + lane]), Elem<DT>::to_f(h[t * dpad + whole + lane]), z[r][t]);
+            }
+        } else {
+#pragma unroll 4
+            for (int64_t c = lane; c < a.D; c += 32)
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) z[r][t] = fmaf(Elem<DT>::to_f(w[r][c]), Elem<DT>::to_f(h[t * dpad + c]), z[r][t]);
+        }
+        // The four rows' sums over the lanes, the rows dealt out on the way: lanes 8r to 8r + 7 end with
+        // row r, and keep the statistics of the rows they have had.
+        const bool up = lane & 16, right = lane & 8;
+        const int64_t v = v0 + (lane >> 3);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float a0 = up ? z[2][t] : z[0][t], a1 = up ? z[3][t] : z[1][t];
+            const float b0 = a0 + __shfl_xor_sync(0xffffffffu, up ? z[0][t] : z[2][t], 16);
+            const float b1 = a1 + __shfl_xor_sync(0xffffffffu, up ? z[1][t] : z[3][t], 16);
+            float x = (right ? b1 : b0) + __shfl_xor_sync(0xffffffffu, right ? b0 : b1, 8);
+#pragma unroll
+            for (int o = 4; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (v < a.V) {
+                if (y[t] == v && (lane & 7) == 0) a.ztarget[t] = x;
+                st[t] = join_pairs(st[t], x == -INFINITY ? make_float2(-INFINITY, 0.f) : make_float2(x, 1.f));
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int o = 8; o <= 16; o *= 2)
+            st[t] = join_pairs(st[t], make_float2(__shfl_xor_sync(0xffffffffu, st[t].x, o), __shfl_xor_sync(0xffffffffu, st[t].y, o)));
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        if (lane == 0) joined[warp][t] = st[t];
+    __syncthreads();
+    if (tid < NT && tid < a.T) {
+        float2 q = joined[0][tid];
+        for (int w = 1; w < kFewThreads / 32; ++w) q = join_pairs(q, joined[w][tid]);
+        a.part[static_cast<int64_t>(tid) * gridDim.x + blockIdx.x] = q;
+    }
+}
+
+__global__ void __launch_bounds__(256) few_join_kernel(FewArgs a)
+{
+    __shared__ float2 sh[256];
+    const int t = blockIdx.x, tid = threadIdx.x;
+    wait_for_previous();
+    const int64_t y = load_id(a.targets, a.id_bytes, t);
+    if (y < 0 || y >= a.V || y == a.ignore) {
+        if (tid == 0) {
+            if (y != a.ignore) atomicOr(a.status, kErrId);
+            a.loss[t] = 0.f;
+            a.lse[t] = 0.f;
+        }
+        return;
+    }
+    float2 q = make_float2(-INFINITY, 0.f);
+    for (int i = tid; i < a.ctas; i += 256) q = join_pairs(q, a.part[static_cast<int64_t>(t) * a.ctas + i]);
+    sh[tid] = q;
+    for (int o = 128; o; o >>= 1) {
+        __syncthreads();
+        if (tid < o) sh[tid] = join_pairs(sh[tid], sh[tid + o]);
+    }
+    if (tid == 0) {
+        const float l = sh[0].x + logf(sh[0].y);
+        a.lse[t] = l;
+        a.loss[t] = l - a.ztarget[t];
+    }
+}
+
+bool few_tokens(int64_t T, int64_t D)
+{
+    return T <= kFewTokens && T * round_up(D, 8) <= kFewElements;
+}
+
 struct Call {
     const void* hidden;
     int64_t hs;
@@ -1020,6 +1175,27 @@ ddp_status check(const char* fn, const Call& c, const void* workspace, int64_t w
         return fail(DDP_E_INVAL, "%s: workspace of %lld bytes (16-byte aligned), needs %lld", fn,
                     static_cast<long long>(workspace ? workspace_bytes : 0), static_cast<long long>(need));
     return DDP_OK;
+}
+
+template <int DT, int NT> cudaError_t launch_few_as(const FewArgs& a, bool vec, cudaStream_t s)
+{
+    const int smem = NT * static_cast<int>(round_up(a.D, 8)) * 2;
+    static std::atomic<bool> ready[ddp::kMaxDevices] = {};
+    const int dev = ddp::current_device();
+    if (dev < 0 || !ready[dev].load(std::memory_order_relaxed)) {
+        for (auto k : {few_kernel<DT, NT, true>, few_kernel<DT, NT, false>}) {
+            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kFewElements);
+            if (e != cudaSuccess) return e;
+        }
+        if (dev >= 0) ready[dev].store(true, std::memory_order_relaxed);
+    }
+    const cudaError_t e = launch_chained(vec ? few_kernel<DT, NT, true> : few_kernel<DT, NT, false>,
+                                         dim3(static_cast<unsigned>(a.ctas)), kFewThreads, smem, s, a);
+    return e != cudaSuccess ? e : launch_chained(few_join_kernel, dim3(static_cast<unsigned>(a.T)), 256, 0, s, a);
+}
+template <int DT> cudaError_t launch_few(const FewArgs& a, bool vec, cudaStream_t s)
+{
+    return a.T == 1 ? launch_few_as<DT, 1>(a, vec, s) : launch_few_as<DT, kFewTokens>(a, vec, s);
 }
 
 bool needs_copy(const Call& c) { return !aligned16(c.weight) || c.ws % 8 != 0; }
@@ -1061,6 +1237,13 @@ cudaError_t launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, in
 
 template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* w, int* status, float* loss, float* lse, cudaStream_t s)
 {
+    if (few_tokens(c.T, c.D)) {
+        FewArgs f{c.hidden, c.hs, c.weight, c.ws, c.V, c.D, c.targets, c.id_bytes, static_cast<int32_t>(c.T), c.ignore,
+                  reinterpret_cast<float2*>(w + sp.part), reinterpret_cast<float*>(w + sp.ztarget), loss, lse, 0, status};
+        const int64_t want = (c.V + kFewRows * (kFewThreads / 32) - 1) / (kFewRows * (kFewThreads / 32));
+        f.ctas = static_cast<int32_t>(std::min<int64_t>({want, kFewPerSm * ddp::device_sm_count(), kMaxFewCtas}));
+        return launch_few<DT>(f, aligned16(c.weight) && c.ws % 8 == 0, s);
+    }
     PrepArgs a{};
     a.loss = loss;
     a.lse_out = lse;

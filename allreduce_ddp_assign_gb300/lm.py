@@ -209,6 +209,7 @@ class VocabLoss:
         self.ignore_index, self.piece = int(ignore_index), int(piece)
         self._same = (dtype,)
         self._wide = (dtype, torch.float32)
+        self._sizes = {}
 
     def _inputs(self, hidden, weight, targets):
         n = targets.numel()
@@ -216,7 +217,12 @@ class VocabLoss:
         hs = _rows(hidden, "hidden", n, self.dim, self._same)
         ws = _rows(weight, "weight", self.vocab, self.dim, self._same)
         at = weight.data_ptr()
-        sizes = ddp_vocab_loss_workspace(n, self.vocab, self.dim, self.piece, at % 16 == 0 and ws % 8 == 0)
+        key = n, at % 16 == 0 and ws % 8 == 0
+        sizes = self._sizes.get(key)
+        if sizes is None:
+            if len(self._sizes) >= 64:
+                self._sizes.clear()
+            sizes = self._sizes[key] = ddp_vocab_loss_workspace(n, self.vocab, self.dim, self.piece, key[1])
         return n, id_bytes, hs, ws, at, sizes
 
     def forward(self, hidden, weight, targets, stream=None):
@@ -227,7 +233,7 @@ class VocabLoss:
         n, id_bytes, hs, ws, at, (size, _) = self._inputs(hidden, weight, targets)
         both = torch.empty((2, n), dtype=torch.float32, device=weight.device)
         scratch = torch.empty(size, dtype=torch.uint8, device=weight.device)
-        loss, lse = both.unbind(0)
+        loss, lse = both[0], both[1]
         _check(lib().ddp_vocab_loss_forward(hidden.data_ptr(), hs, at, ws, self.dtype, n, self.vocab, self.dim,
                                             targets.data_ptr(), id_bytes, self.ignore_index, loss.data_ptr(),
                                             lse.data_ptr(), scratch.data_ptr(), size,

@@ -932,6 +932,7 @@ ddp_status ddp_clip_grads(const void* const* grads, void* const* out, const int6
  * ddp_embedding_forward -- out[t] = scale * weight[ids[t]] for ntokens tokens.
  * A token whose id is outside [0, vocab) gets a row of zeros (and bit 1 of
  * ddp_lm_status).  weight and out are `dtype`.
+ * ntokens and vocab < 2^31, dim < 2^28.
  * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, a stride below dim, an
  * unknown dtype or id_bytes, a NULL pointer with ntokens > 0); DDP_E_CUDA.
  */
@@ -953,7 +954,6 @@ ddp_status ddp_embedding_workspace(int64_t ntokens, int64_t vocab, int64_t dim, 
  *   grad_out     DEVICE dtype [ntokens x dim], rows grad_stride apart.
  *   grad_weight  DEVICE gw_dtype [vocab x dim], rows gw_stride apart; gw_dtype is
  *                dtype or DDP_F32 (a main_grad segment).
- * ntokens < 2^31.
  * Errors: as ddp_embedding_forward; DDP_E_INVAL for another gw_dtype or too
  * small a workspace.
  */
