@@ -219,15 +219,28 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
     __syncthreads();
     // rows in 16-byte vectors where the tensors allow it
     const int64_t vecs = a.vec ? a.dpad / 8 : 0;
-    for (int64_t i = tid; i < vecs * (t1 - t0); i += kPrepThreads) {
-        const int r = static_cast<int>(i / vecs);
-        const int64_t c = (i - r * vecs) * 8;
-        const int at = place[r];
-        if (at >= 0)
-            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(at) * a.dpad + c) =
-                *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs + c);
-        else if (a.gh)
-            *reinterpret_cast<uint4*>(a.gh + static_cast<int64_t>(t0 + r) * a.ghs + c) = make_uint4(0, 0, 0, 0);
+    const int rows = t1 - t0;
+    for (int64_t i = tid; i < vecs * rows; i += 4 * kPrepThreads) {
+        uint4 v[4];
+        uint16_t* to[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t k = i + j * kPrepThreads;
+            to[j] = nullptr;
+            if (k >= vecs * rows) continue;
+            const int r = static_cast<int>(static_cast<uint32_t>(k) / static_cast<uint32_t>(vecs));
+            const int64_t c = (k - r * vecs) * 8;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (place[r] >= 0) {
+                to[j] = a.out + static_cast<int64_t>(place[r]) * a.dpad + c;
+                v[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs + c);
+            } else if (a.gh) {
+                to[j] = a.gh + static_cast<int64_t>(t0 + r) * a.ghs + c;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (to[j]) *reinterpret_cast<uint4*>(to[j]) = v[j];
     }
     if (!a.vec) {
         for (int i = warp; i < t1 - t0; i += kPrepThreads / 32) {
