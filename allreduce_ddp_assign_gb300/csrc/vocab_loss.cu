@@ -26,8 +26,10 @@ constexpr int kRowTile = 256;   // rows of the gathered arrays are padded to thi
 constexpr int kPrepThreads = 256;
 constexpr int kFewTokens = 2;      // up to so many the forward pass goes without matrix products
 constexpr int kMaxFewCtas = 1024;
-// elements of G that are held at a time: 268 MB
-constexpr int64_t kPieceElements = int64_t{1} << 27;
+// Elements of G that are held at a time: 537 MB.  More pieces are more launches, which cost
+// about 8 us each at their ends (8192 x 50257 x 768: 1583 us with half of it, 1565; the masked
+// step at 30522 x 1024: 367 and 340).
+constexpr int64_t kPieceElements = int64_t{1} << 28;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // G's scale in fp16: its largest magnitude, 1 after the division by the largest
