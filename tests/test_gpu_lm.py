@@ -334,7 +334,7 @@ def test_embedding_offsets_beyond_32_bits():
 LOSS = [  # tokens, vocab, dim, ignored share, aligned
     (1, 1, 1, 0.0, True), (1, 50257, 768, 0.0, True), (3, 7, 5, 0.0, True), (17, 256, 64, 0.0, True),
     (130, 1000, 72, 0.3, True), (257, 513, 257, 0.1, True), (300, 2049, 128, 0.9, True), (200, 700, 100, 0.2, False),
-    (1000, 3001, 192, 0.0, True), (64, 20000, 320, 0.5, True), (520, 4096, 520, 0.15, True),
+    (1000, 3001, 192, 0.0, True), (2, 5000, 200, 0.0, True), (2, 300, 77, 0.5, False), (64, 20000, 320, 0.5, True), (520, 4096, 520, 0.15, True),
 ]
 
 
@@ -428,6 +428,19 @@ def test_loss_backward(T, V, dim, ignored, aligned, dt, piece):
     assert_guard(b2, gw)
     gh2, gw2 = f.backward(h, w, y, lse, gl)
     assert torch.equal(gh, gh2) and torch.equal(gw, gw2)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,ignored", [(100, 0.0), (600, 0.8), (2, 0.0)])
+def test_loss_backward_in_long_pieces(dt, T, ignored):
+    """Few rows and long pieces: the hidden states' gradient is split along each piece and summed over the pieces."""
+    V, dim = 9001, 264
+    h, w, y, valid = loss_case(60, T, V, dim, ignored, dt)
+    f = lm.VocabLoss(V, dim, dt, piece=4096)
+    _, lse = f.forward(h, w, y)
+    gl = torch.rand(T, generator=gen(61), device=DEV)
+    gh, gw = f.backward(h, w, y, lse, gl)
+    check_grads(h, w, y, valid, gl, gh, gw, torch.zeros_like(gw), dt)
 
 
 @pytest.mark.parametrize("dt", [BF16, F16])
