@@ -95,34 +95,36 @@ template <bool INF> __device__ __forceinline__ double join(double a, double b)
 // N values (at most 32) into the sum of squares, in fp32 and then once in fp64, or into the largest magnitude.
 template <bool INF, int N> __device__ __forceinline__ void add_values(double& acc, const float (&x)[N])
 {
-    float m = 0.f;
+    // (four chains each: the loads of the next values wait for these)
+    float mm[4] = {0.f, 0.f, 0.f, 0.f};
     if (INF) {
         float bad = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            m = fmaxf(m, fabsf(x[j]));
+            mm[j & 3] = fmaxf(mm[j & 3], fabsf(x[j]));
             bad = x[j] != x[j] ? x[j] : bad;
         }
-        acc = join<true>(acc, bad != bad ? bad : m);
+        acc = join<true>(acc, bad != bad ? bad : fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])));
         return;
     }
-    float s0 = 0.f, s1 = 0.f;
+    float ss[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        m = fmaxf(m, fabsf(x[j]));
-        if (j & 1) s1 = fmaf(x[j], x[j], s1);
-        else s0 = fmaf(x[j], x[j], s0);
+        mm[j & 3] = fmaxf(mm[j & 3], fabsf(x[j]));
+        ss[j & 3] = fmaf(x[j], x[j], ss[j & 3]);
     }
+    const float m = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3]));
+    float s = (ss[0] + ss[1]) + (ss[2] + ss[3]);
     if (fp32_square_range(m)) {
-        acc += static_cast<double>(s0 + s1);
-    } else if (!(s0 + s1 == 0.f && m == 0.f)) {
+        acc += static_cast<double>(s);
+    } else if (!(s == 0.f && m == 0.f)) {
         // moved into the range by a power of two, whose square is taken out again in fp64
         const bool large = m > 1.f;
         const float f = large ? 0x1p-68f : 0x1p100f;
-        s0 = 0.f;
+        s = 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) s0 = fmaf(x[j] * f, x[j] * f, s0);
-        acc += static_cast<double>(s0) * (large ? 0x1p136 : 0x1p-200);
+        for (int j = 0; j < N; ++j) s = fmaf(x[j] * f, x[j] * f, s);
+        acc += static_cast<double>(s) * (large ? 0x1p136 : 0x1p-200);
     }
 }
 

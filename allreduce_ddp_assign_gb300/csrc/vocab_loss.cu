@@ -1013,12 +1013,15 @@ combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, in
 // forward for a few tokens
 // ---------------------------------------------------------------------------
 // HBM-bound: the weight is read once, a warp takes four of its rows at a time and
-// multiplies them with every token's hidden state, which shared memory holds.  At 50257 x
+// multiplies them with every token's hidden state, which shared memory holds.  One CTA an
+// SM, with 128 KB of the weight on its way all the time.  At 50257 x
 // 768 one token takes 29 us (50 on the tensor cores), two take 38 (50), four 66 (52).
 constexpr int kFewElements = 32768;  // of hidden states in shared memory
 constexpr int kFewThreads = 256;
-constexpr int kFewRows = 4;  // (the reduction over the lanes is written for four)
-constexpr int kFewPerSm = 3;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewRows = 4;        // (the reduction over the lanes is written for four)
+constexpr int kFewStages = 8;      // parts on their way to a warp: four rows' 256 values, 2 KB
+constexpr int kFewStageBytes = kFewRows * 512;
 
 struct FewArgs {
     const void* hidden;
@@ -1036,12 +1039,13 @@ struct FewArgs {
     int* status;
 };
 
-template <int DT, int NT, bool VEC> __global__ void __launch_bounds__(kFewThreads, kFewPerSm) few_kernel(FewArgs a)
+template <int DT, int NT, bool VEC> __global__ void __launch_bounds__(kFewThreads) few_kernel(FewArgs a)
 {
     using T = typename Elem<DT>::T;
     extern __shared__ __align__(16) uint8_t few_smem[];
-    __shared__ float2 joined[kFewThreads / 32][NT];
-    T* h = reinterpret_cast<T*>(few_smem);  // [NT][dpad], zeros past the row's end
+    __shared__ float2 joined[kFewWarps][NT];
+    uint8_t* ring = few_smem + (threadIdx.x >> 5) * kFewStages * kFewStageBytes;
+    T* h = reinterpret_cast<T*>(few_smem + (VEC ? kFewWarps * kFewStages * kFewStageBytes : 0));  // [NT][dpad], zeros past the row's end
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t dpad = (a.D + 7) / 8 * 8;
     wait_for_previous();
@@ -1056,20 +1060,49 @@ template <int DT, int NT, bool VEC> __global__ void __launch_bounds__(kFewThread
     float2 st[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) st[t] = make_float2(-INFINITY, 0.f);
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
-    for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp) * kFewRows; v0 < a.V; v0 += warps * kFewRows) {
-        float z[kFewRows][NT] = {};
-        // rows past the last word read the last word's
-        const T* w[kFewRows];
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kFewWarps, w0 = static_cast<int64_t>(blockIdx.x) * kFewWarps + warp;
+    // Part i of this warp: rows [v, v + 4) with v = 4 (w0 + warps (i / parts)), values [256 (i % parts), ...).
+    // A row's part goes straight to shared memory, several parts ahead, zeros past the row's end;
+    // each lane reads back only what it copied itself.
+    const int parts = static_cast<int>((a.D + 255) / 256);
+    int64_t ahead_v = w0 * kFewRows;
+    int ahead_c = 0, ahead_s = 0;
+    auto copy_part = [&]() {
+        if (ahead_v < a.V) {
+            const int64_t c = ahead_c * 256 + lane * 8;
+            const int bytes = static_cast<int>(max(int64_t{0}, min(int64_t{16}, (a.D - c) * 2)));
 #pragma unroll
-        for (int r = 0; r < kFewRows; ++r) w[r] = static_cast<const T*>(a.weight) + min(v0 + r, a.V - 1) * a.ws;
+            for (int r = 0; r < kFewRows; ++r) {
+                // rows past the last word copy the last word's
+                const T* src = static_cast<const T*>(a.weight) + min(ahead_v + r, a.V - 1) * a.ws + (bytes ? c : 0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(ring + ahead_s * kFewStageBytes + r * 512 + lane * 16)),
+                             "l"(src), "r"(bytes)
+                             : "memory");
+            }
+            if (++ahead_c == parts) {
+                ahead_c = 0;
+                ahead_v += warps * kFewRows;
+            }
+            ahead_s = ahead_s + 1 == kFewStages ? 0 : ahead_s + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (VEC)
+        for (int i = 0; i < kFewStages - 1; ++i) copy_part();
+    int stage = 0;
+    for (int64_t v0 = w0 * kFewRows; v0 < a.V; v0 += warps * kFewRows) {
+        float z[kFewRows][NT] = {};
         if (VEC) {
-            const int64_t whole = a.D / 8 * 8;
-#pragma unroll 3
-            for (int64_t c = lane * 8; c < whole; c += 256) {
+            for (int p = 0; p < parts; ++p) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
                 Vec<DT> x[kFewRows];
 #pragma unroll
-                for (int r = 0; r < kFewRows; ++r) x[r] = *reinterpret_cast<const Vec<DT>*>(w[r] + c);
+                for (int r = 0; r < kFewRows; ++r)
+                    x[r] = *reinterpret_cast<const Vec<DT>*>(ring + stage * kFewStageBytes + r * 512 + lane * 16);
+                stage = stage + 1 == kFewStages ? 0 : stage + 1;
+                copy_part();
+                const int64_t c = p * 256 + lane * 8;
+                if (c >= a.D) continue;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const Vec<DT> q = *reinterpret_cast<const Vec<DT>*>(h + t * dpad + c);
@@ -1079,14 +1112,10 @@ template <int DT, int NT, bool VEC> __global__ void __launch_bounds__(kFewThread
                         for (int r = 0; r < kFewRows; ++r) z[r][t] = fmaf(Elem<DT>::to_f(x[r].v[j]), Elem<DT>::to_f(q.v[j]), z[r][t]);
                 }
             }
-            if (whole + lane < a.D) {
-#pragma unroll
-                for (int r = 0; r < kFewRows; ++r)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        z[r][t] = fmaf(Elem<DT>::to_f(w[r][whole + lane]), Elem<DT>::to_f(h[t * dpad + whole + lane]), z[r][t]);
-            }
         } else {
+            const T* w[kFewRows];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) w[r] = static_cast<const T*>(a.weight) + min(v0 + r, a.V - 1) * a.ws;
 #pragma unroll 4
             for (int64_t c = lane; c < a.D; c += 32)
 #pragma unroll
@@ -1123,7 +1152,7 @@ template <int DT, int NT, bool VEC> __global__ void __launch_bounds__(kFewThread
     __syncthreads();
     if (tid < NT && tid < a.T) {
         float2 q = joined[0][tid];
-        for (int w = 1; w < kFewThreads / 32; ++w) q = join_pairs(q, joined[w][tid]);
+        for (int w = 1; w < kFewWarps; ++w) q = join_pairs(q, joined[w][tid]);
         a.part[static_cast<int64_t>(tid) * gridDim.x + blockIdx.x] = q;
     }
 }
@@ -1194,12 +1223,13 @@ ddp_status check(const char* fn, const Call& c, const void* workspace, int64_t w
 
 template <int DT, int NT> cudaError_t launch_few_as(const FewArgs& a, bool vec, cudaStream_t s)
 {
-    const int smem = NT * static_cast<int>(round_up(a.D, 8)) * 2;
+    constexpr int kRing = kFewWarps * kFewStages * kFewStageBytes;
+    const int smem = NT * static_cast<int>(round_up(a.D, 8)) * 2 + (vec ? kRing : 0);
     static std::atomic<bool> ready[ddp::kMaxDevices] = {};
     const int dev = ddp::current_device();
     if (dev < 0 || !ready[dev].load(std::memory_order_relaxed)) {
         for (auto k : {few_kernel<DT, NT, true>, few_kernel<DT, NT, false>}) {
-            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kFewElements);
+            const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kFewElements + kRing);
             if (e != cudaSuccess) return e;
         }
         if (dev >= 0) ready[dev].store(true, std::memory_order_relaxed);
@@ -1255,8 +1285,8 @@ template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* 
     if (few_tokens(c.T, c.D)) {
         FewArgs f{c.hidden, c.hs, c.weight, c.ws, c.V, c.D, c.targets, c.id_bytes, static_cast<int32_t>(c.T), c.ignore,
                   reinterpret_cast<float2*>(w + sp.part), reinterpret_cast<float*>(w + sp.ztarget), loss, lse, 0, status};
-        const int64_t want = (c.V + kFewRows * (kFewThreads / 32) - 1) / (kFewRows * (kFewThreads / 32));
-        f.ctas = static_cast<int32_t>(std::min<int64_t>({want, kFewPerSm * ddp::device_sm_count(), kMaxFewCtas}));
+        const int64_t want = (c.V + kFewRows * kFewWarps - 1) / (kFewRows * kFewWarps);
+        f.ctas = static_cast<int32_t>(std::min<int64_t>({want, ddp::device_sm_count(), kMaxFewCtas}));
         return launch_few<DT>(f, aligned16(c.weight) && c.ws % 8 == 0, s);
     }
     PrepArgs a{};
