@@ -152,6 +152,15 @@ __device__ __forceinline__ int block_sum(int v, int* sh)
     return r;
 }
 
+// Values [c, c + 8) of a row that may start anywhere, zeros past its end.
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t dim)
+{
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < dim ? __ldg(row + c + j) : 0;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
 // Every CTA counts the tokens with a target before its own slab, and all of them, itself.
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
 {
@@ -245,16 +254,15 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
             if (to[j]) *reinterpret_cast<uint4*>(to[j]) = v[j];
     }
     if (!a.vec) {
-        for (int i = warp; i < t1 - t0; i += kPrepThreads / 32) {
-            const int at = place[i];
-            const uint16_t* src = static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + i) * a.hs;
-            if (at >= 0) {
-                uint16_t* dst = a.out + static_cast<int64_t>(at) * a.dpad;
-                for (int64_t c = lane; c < a.dpad; c += 32) dst[c] = c < a.dim ? src[c] : 0;
-            } else if (a.gh) {
-                uint16_t* dst = a.gh + static_cast<int64_t>(t0 + i) * a.ghs;
-                for (int64_t c = lane; c < a.dim; c += 32) dst[c] = 0;
-            }
+        const int64_t all_vecs = a.dpad / 8;
+        for (int64_t i = tid; i < all_vecs * rows; i += kPrepThreads) {
+            const int r = static_cast<int>(i / all_vecs);
+            const int64_t c = (i - r * all_vecs) * 8;
+            if (place[r] >= 0)
+                *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(place[r]) * a.dpad + c) =
+                    load8(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs, c, a.dim);
+            else if (a.gh)
+                for (int64_t k = c; k < min(c + 8, a.dim); ++k) a.gh[static_cast<int64_t>(t0 + r) * a.ghs + k] = 0;
         }
     }
     // rows up to the tile's end are zeros (past the T-th the copies supply them): they are terms of dW's sums
@@ -264,12 +272,24 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
             *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(r) * a.dpad + c) = make_uint4(0, 0, 0, 0);
 }
 
+// An aligned copy of rows that start anywhere: a thread gathers 8 values at a time, the
+// cache line stays in L1 for the eight loads.
 __global__ void __launch_bounds__(256)
 copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, uint16_t* out, int64_t dpad)
 {
     wait_for_previous();
-    for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x)
-        for (int64_t c = threadIdx.x; c < dpad; c += blockDim.x) out[v * dpad + c] = c < dim ? w[v * ws + c] : 0;
+    const int64_t vecs = dpad / 8, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < vocab * vecs; i += 2 * step) {
+        uint4 x[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t k = i + j * step, v = k / vecs;
+            if (k < vocab * vecs) x[j] = load8(w + v * ws, (k - v * vecs) * 8, dim);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (i + j * step < vocab * vecs) *reinterpret_cast<uint4*>(out + (i + j * step) * 8) = x[j];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -471,20 +491,18 @@ __device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, c
                 for (int j = 0; j < 32; ++j) z = y - n == j ? c[j] : z;
                 p.ztarget[m] = z;
             }
-            float cm = c[0];
+            // (four chains: with little k the epilogue is what a tile takes)
+            float cm[4] = {c[0], c[1], c[2], c[3]};
 #pragma unroll
-            for (int j = 1; j < 32; ++j) cm = fmaxf(cm, c[j]);
-            const float top = fmaxf(mx, cm);
+            for (int j = 4; j < 32; ++j) cm[j & 3] = fmaxf(cm[j & 3], c[j]);
+            const float top = fmaxf(fmaxf(mx, fmaxf(cm[0], cm[1])), fmaxf(cm[2], cm[3]));
             if (top != -INFINITY) {  // all of them minus infinity: they add nothing
                 const float shift = top * kLog2e;
                 s *= mx == -INFINITY ? 0.f : pow2(mx * kLog2e - shift);
-                float a0 = 0.f, a1 = 0.f;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    a0 += pow2(fmaf(c[j], kLog2e, -shift));
-                    a1 += pow2(fmaf(c[j + 1], kLog2e, -shift));
-                }
-                s += a0 + a1;
+                for (int j = 0; j < 32; ++j) part[j & 3] += pow2(fmaf(c[j], kLog2e, -shift));
+                s += (part[0] + part[1]) + (part[2] + part[3]);
                 mx = top;
             } else {
 #pragma unroll
@@ -1272,7 +1290,7 @@ cudaError_t launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, in
     *ws = c.ws;
     if (needs_copy(c)) {
         uint16_t* dst = reinterpret_cast<uint16_t*>(w + sp.weight);
-        e = launch_chained(copy_weight_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(c.V, 1 << 20))), 256, 0, s,
+        e = launch_chained(copy_weight_kernel, dim3(static_cast<unsigned>(8 * ddp::device_sm_count())), 256, 0, s,
                            static_cast<const uint16_t*>(c.weight), c.ws, c.V, c.D, dst, sp.dpad);
         *weight = dst;
         *ws = sp.dpad;
