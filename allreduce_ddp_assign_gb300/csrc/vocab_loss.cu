@@ -63,7 +63,10 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     const int64_t vpad = round_up(V, 256);
     // G in two buffers of half the words asked for, one filled while the other is read
     if (piece <= 0) piece = std::max<int64_t>(2048, kPieceElements / s.tpad);
-    s.piece = piece >= vpad ? vpad : std::min(vpad, round_up(piece, 512) / 2);
+    const int64_t most = piece >= vpad ? vpad : std::min(vpad, round_up(piece, 512) / 2);
+    // equal pieces: the last one is a launch of its own, which a few words would leave idle
+    s.pieces = (V + most - 1) / most;
+    s.piece = std::min(most, round_up((V + s.pieces - 1) / s.pieces, 256));
     s.pieces = backward ? (V + s.piece - 1) / s.piece : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -80,7 +83,7 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     if (backward) {
         s.ratio = take(4 * s.tpad);
         s.lse = take(4 * s.tpad);
-        s.grad_bytes = round_up(2 * s.tpad * s.piece, 256);
+        s.grad_bytes = round_up(2 * s.tpad * most, 256);
         s.grad = take(s.grad_bytes * std::min<int64_t>(s.pieces, 2));
         // splits x rows: at most (kSplitTiles / nt + mt) tiles of rows
         const int64_t nt = (D + 255) / 256;
