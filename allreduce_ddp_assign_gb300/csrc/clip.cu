@@ -10,6 +10,12 @@
 // HBM-bound: one pass reads every element for the norm, a second reads and writes
 // it; the factor is known only when the last element has been read.  The second
 // pass goes backwards, where the first one's last elements are still in L2.
+//
+// Measured on a GB300: 334M fp32 elements in 385 tensors 657 us (4.0 GB, 6.1 TB/s: the
+// norm's pass 210 us, 6.3 TB/s); 124M bf16 in 193 tensors 151 us (0.74 GB, 4.9 TB/s; the
+// norm's pass 59 us, 4.2 TB/s, where half of the time goes into the squares between the
+// loads); 0.33M fp32 in 17 tensors 13 us, which is two launches and their dependent reads.
+// Sums of squares: fp32 over at most 32 values, fp64 beyond.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

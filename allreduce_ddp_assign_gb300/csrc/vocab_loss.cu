@@ -12,6 +12,12 @@
 // Tokens without a target are left out first: the hidden states of the others are
 // gathered into consecutive rows, so masked-word training pays for the masked
 // words only and nothing an ignored row holds can reach a result.
+//
+// Bound by the tensor cores: 2 T V D operations forward, 8 T V D for a step (6 without the
+// second z).  Measured on a GB300 (2 T V D = 632 GFLOP at 8192 tokens x 50257 words x 768,
+// bf16): z and its statistics 343 us, 1.84 PFLOP/s or 0.96 of the rate cuBLAS reaches
+// here; a step 1.55 ms.  At 4096 x 131072 x 4096 a launch of dH, dW and the next G runs
+// at 1.95 PFLOP/s and the step, seconds long, at what the power limit leaves (1.67).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -164,7 +170,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t d
     return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
-// Every CTA counts the tokens with a target before its own slab, and all of them, itself.
+// Every CTA counts the tokens with a target before its own slab, and all of them, itself:
+// no launch of its own for the places, and 8 bytes a token and CTA from L2.  Bound by the
+// latency of four dependent reads; 13 us for 8192 rows of 768 (25 MB) with cold caches.
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
 {
     __shared__ int sh[kPrepThreads / 32];
@@ -309,6 +317,14 @@ copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, ui
 // A launch runs one or several products, one a use at most, their tiles one after the other, longest
 // first: with dH and dW of one piece of the vocabulary comes G of the next, whose
 // short tiles fill what the long ones leave idle at the end.
+//
+// Why so: a CTA's 128 x 256 share of a tile needs 32 KB of operands for 512 cycles of
+// products; alone, without the pair, it would need 48 KB, more than an SM gets from L2 in
+// that time.  Six stages are 192 KB; four to six made no difference.  What did, at 8192 x
+// 50257 x 768: barriers that publish nothing (438 -> 383 us forward), the code written out
+// for each use (466 -> 443), tiles worked out by a warp of their own (500 -> 466), reading
+// ahead what dH and dW add to (masked step 480 -> 402).  Where k is short the epilogue is
+// the bound: 2.1 us a tile at 128 values of k, twice what its exponentials take.
 // what becomes of C, in the order in which a launch runs them
 enum Use { USE_DH, USE_DW, USE_GRAD, USE_STATS, kUses };
 
@@ -858,7 +874,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
     if (warp == 9) tmem_free(tmem, 512);
 }
 
-// dH where its tiles were split along the vocabulary: the splits' sums, in order
+// dH where its tiles were split along the vocabulary: the splits' sums, in order.  HBM-bound;
+// it returns at once where there were no splits.
 template <int DT>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Product p, const int32_t* count)
 {
@@ -966,7 +983,9 @@ template <int DT> cudaError_t launch_products(const Batch& batch, cudaStream_t s
     return cudaLaunchKernelEx(&cfg, product_kernel<DT>, batch);
 }
 
-// joins the (maximum, sum) pairs of each gathered row: 32 threads a row, in a fixed order
+// Joins the (maximum, sum) pairs of each gathered row, m = max m_i and s = sum s_i 2^((m_i - m) log2 e):
+// 32 threads a row and eight rows a CTA, so that 64 bytes of neighbouring rows' pairs are
+// read together and one row alone is still read by 32 threads.  In a fixed order.
 constexpr int kJoinRows = 8;
 __device__ __forceinline__ float2 join_pairs(float2 a, float2 b)
 {
@@ -1036,7 +1055,8 @@ combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, in
 // HBM-bound: the weight is read once, a warp takes four of its rows at a time and
 // multiplies them with every token's hidden state, which shared memory holds.  One CTA an
 // SM, with 128 KB of the weight on its way all the time.  At 50257 x
-// 768 one token takes 29 us (50 on the tensor cores), two take 38 (50), four 66 (52).
+// 768 with cold caches one token takes 27 us (50 on the tensor cores; the read alone 17.5
+// us, 4.4 TB/s) and two 30; four took 66 (52) with registers instead of the ring.
 constexpr int kFewElements = 32768;  // of hidden states in shared memory
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
