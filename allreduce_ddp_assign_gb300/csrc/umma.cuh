@@ -39,24 +39,10 @@ __device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
 }
-// The same from afar, and a plain arrival (`b`: an address in the cluster's shared
-// memory).  Neither publishes memory to the cluster: what they announce is a count of
-// bytes, or that registers have been read.  (A release at cluster scope would wait for
-// all of the thread's stores to HBM.)
-__device__ __forceinline__ void bar_expect_cluster(uint32_t b, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
-}
+// `b` is an address in the cluster's shared memory
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t b)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
-}
-// 16 bytes into a CTA's shared memory, counted on that CTA's barrier (addresses in the cluster's shared memory)
-__device__ __forceinline__ void store_cluster(uint32_t a, int4 v, uint32_t bar)
-{
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
-                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
-                 : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity)
 {
@@ -70,6 +56,19 @@ __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity)
         : "memory");
     return done != 0;
 }
+// The same where the other CTA's threads arrive.
+__device__ __forceinline__ bool bar_try_cluster(uint32_t b, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(b), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ uint64_t clock_ns()
 {
     uint64_t t;
@@ -77,15 +76,17 @@ __device__ __forceinline__ uint64_t clock_ns()
     return t;
 }
 
-// A wait that gives up: after about 2 s, or as soon as another wait of the CTA has.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile int* dead)
+// A wait that gives up: after about 2 s, or as soon as another wait of the CTA has.  Time
+// is the SM's own cycle count, which only goes forward.
+constexpr long long kWaitLimitCycles = 4000000000ll;
+template <bool CLUSTER = false> __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile int* dead)
 {
-    if (bar_try(b, parity)) return true;
-    const uint64_t t0 = clock_ns();
+    auto done = [&]() { return CLUSTER ? bar_try_cluster(b, parity) : bar_try(b, parity); };
+    if (done()) return true;
+    const long long t0 = clock64();
     for (uint32_t i = 1; i < (1u << 28); ++i) {
-        if (bar_try(b, parity)) return true;
-        if ((i & 255u) == 0 && (*dead || clock_ns() - t0 > kWaitLimitNs)) break;
+        if (done()) return true;
+        if ((i & 255u) == 0 && (*dead || clock64() - t0 > kWaitLimitCycles)) break;
     }
     *dead = 1;
     return false;

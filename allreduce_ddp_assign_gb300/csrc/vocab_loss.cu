@@ -16,8 +16,8 @@
 // Bound by the tensor cores: 2 T V D operations forward, 8 T V D for a step (6 without the
 // second z).  Measured on a GB300 (2 T V D = 632 GFLOP at 8192 tokens x 50257 words x 768,
 // bf16): z and its statistics 343 us, 1.84 PFLOP/s or 0.96 of the rate cuBLAS reaches
-// here; a step 1.55 ms.  At 4096 x 131072 x 4096 a launch of dH, dW and the next G runs
-// at 1.95 PFLOP/s and the step, seconds long, at what the power limit leaves (1.67).
+// here; a step 1.72 ms.  At 4096 x 131072 x 4096 the step, seconds long, runs at what the
+// power limit leaves (1.67 PFLOP/s).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -54,7 +54,7 @@ __host__ __device__ __forceinline__ int dh_splits(int mt, int nt, int nkb)
 }
 
 struct Space {
-    int64_t count, gmax, next, rows, target, ratio, lse, hidden, part, ztarget, grad, acc, weight, total;
+    int64_t count, gmax, rows, target, ratio, lse, hidden, part, ztarget, grad, acc, weight, total;
     int64_t piece, pieces, ntiles, tpad, dpad, grad_bytes;
 };
 
@@ -82,7 +82,6 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     };
     s.count = take(4);
     s.gmax = take(4);
-    s.next = take(4 * (vpad / 256 + 1));  // a counter for each launch: pieces + 1 at most
     s.rows = take(4 * s.tpad);
     s.target = take(4 * s.tpad);
     s.hidden = take(2 * s.tpad * s.dpad);
@@ -135,8 +134,6 @@ struct PrepArgs {
     int64_t ghs;
     float g_scale;
     int32_t vec;          // hidden (and gh) in 16-byte vectors
-    int32_t* next;        // tile counters of the launches that follow
-    int32_t nnext;
 };
 
 __device__ __forceinline__ bool token_target(const PrepArgs& a, int t, int64_t* y)
@@ -181,8 +178,6 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = blockIdx.x * a.slab, t1 = min(a.T, t0 + a.slab);
     wait_for_previous();
-    if (blockIdx.x == 0)
-        for (int i = tid; i < a.nnext; i += kPrepThreads) a.next[i] = 0;
     int before = 0, all = 0;
     float gm = 0.f;
     // eight tokens a thread at a time, their loads in flight together
@@ -311,18 +306,18 @@ copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, ui
 // thread of the first CTA issues the products of both.  Per CTA:
 //   warp 8     copies 128 x 64 boxes of A and B into a ring of stages;
 //   warp 9     (first CTA) issues four k = 16 products a stage;
-//   warp 10    (first CTA) claims tiles from a counter and passes them to both CTAs;
 //   warps 0-7  take finished tiles out of tensor memory, which holds two, so that
 //              a tile's epilogue runs under the next tile's products.
 // A launch runs one or several products, one a use at most, their tiles one after the other, longest
 // first: with dH and dW of one piece of the vocabulary comes G of the next, whose
-// short tiles fill what the long ones leave idle at the end.
+// short tiles fill what the long ones leave idle at the end.  A pair takes every
+// npairs-th tile; its warps work the tiles out for themselves and exchange nothing but
+// the barriers' counts.
 //
 // Why so: a CTA's 128 x 256 share of a tile needs 32 KB of operands for 512 cycles of
 // products; alone, without the pair, it would need 48 KB, more than an SM gets from L2 in
-// that time.  Six stages are 192 KB; four to six made no difference.  What did, at 8192 x
-// 50257 x 768: barriers that publish nothing (438 -> 383 us forward), the code written out
-// for each use (466 -> 443), tiles worked out by a warp of their own (500 -> 466), reading
+// that time.  Six stages are 192 KB; four to six made no difference.  What did: the code
+// written out for each use (466 -> 443 us forward at 8192 x 50257 x 768) and reading
 // ahead what dH and dW add to (masked step 480 -> 402).  Where k is short the epilogue is
 // the bound: 2.1 us a tile at 128 values of k, twice what its exponentials take.
 // what becomes of C, in the order in which a launch runs them
@@ -336,8 +331,7 @@ constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kStagingBytes = 4096;      // per epilogue warp: 32 rows of 128 bytes
-constexpr int kSlots = 4;                // claimed tiles on their way to the warps
-constexpr int kProductThreads = 32 * (kEpiWarps + 3);
+constexpr int kProductThreads = 32 * (kEpiWarps + 2);
 constexpr int kProductSmem = kStages * kStageBytes + kEpiWarps * kStagingBytes + 1024;
 constexpr int kGroup = 32;               // tiles along the fast side before the slow side moves on
 
@@ -376,7 +370,6 @@ struct Batch {
     Maps map[kUses];
     Product job[kUses];
     const int32_t* count; // gathered rows: bounds M (STATS, GRAD, DH) or K (DW)
-    int32_t* next;        // tiles claimed beyond each pair's first
     int* status;
 };
 
@@ -399,28 +392,27 @@ __device__ __forceinline__ Shape shape_of(const Product& p, int use, int64_t cou
     return s;
 }
 struct Tile {
-    int32_t use, m, n, split, kb0, kb1;  // use < 0: no more tiles
-    int32_t pad_[2];
+    int32_t use, m, n, split, kb0, kb1;
 };
 // Tile t of a launch.  Tiles that run at the same time share operands: up to kGroup
 // along the side whose operand is the smaller one (the hidden states), then a
 // step along the other, so that the larger one is read from HBM once.
-__device__ __forceinline__ Tile tile_at(int64_t t, const Shape* shapes)
+// (32-bit arithmetic: the copies and the products stand still while their threads think.)
+__device__ __forceinline__ Tile tile_at(uint32_t t, const Shape* shapes)
 {
     Tile r{};
-    while (r.use + 1 < kUses && t >= shapes[r.use].tiles) t -= shapes[r.use++].tiles;
+    while (r.use + 1 < kUses && t >= static_cast<uint32_t>(shapes[r.use].tiles)) t -= static_cast<uint32_t>(shapes[r.use++].tiles);
     const Shape& s = shapes[r.use];
-    const int64_t mn = static_cast<int64_t>(s.mt) * s.nt;
+    const uint32_t mn = static_cast<uint32_t>(s.mt) * s.nt;
     r.split = static_cast<int>(t / mn);
     t -= r.split * mn;
     const bool n_fast = r.use == USE_DW;
-    const int fast = n_fast ? s.nt : s.mt, slow = n_fast ? s.mt : s.nt;
-    const int group = static_cast<int>(t / (static_cast<int64_t>(kGroup) * slow));
-    const int64_t in = t - static_cast<int64_t>(group) * kGroup * slow;
-    const int width = min(kGroup, fast - group * kGroup);
-    const int i = group * kGroup + static_cast<int>(in % width), o = static_cast<int>(in / width);
-    r.m = n_fast ? o : i;
-    r.n = n_fast ? i : o;
+    const uint32_t fast = n_fast ? s.nt : s.mt, slow = n_fast ? s.mt : s.nt;
+    const uint32_t group = t / (kGroup * slow), in = t - group * kGroup * slow;
+    const uint32_t width = min(static_cast<uint32_t>(kGroup), fast - group * kGroup), o = in / width;
+    const uint32_t i = group * kGroup + (in - o * width);
+    r.m = static_cast<int>(n_fast ? o : i);
+    r.n = static_cast<int>(n_fast ? i : o);
     const int per = (s.nkb + s.splits - 1) / s.splits;
     r.kb0 = min(s.nkb, r.split * per);
     r.kb1 = min(s.nkb, r.kb0 + per);
@@ -703,10 +695,9 @@ template <int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Batch batch)
 {
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kSlots];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
     __shared__ Shape shapes[kUses];
     __shared__ uint32_t tmem_base;
-    __shared__ __align__(16) Tile slot_tile[kSlots];
     __shared__ volatile int dead;
     const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_addr(bars);
@@ -716,8 +707,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
     auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
     auto tfull = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
     auto tempty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-    auto sfull = [&](int i) { return bar0 + 8u * (2 * kStages + 4 + i); };
-    auto sempty = [&](int i) { return bar0 + 8u * (2 * kStages + 4 + kSlots + i); };
 
     if (threadIdx.x == 0) {
         dead = 0;
@@ -728,10 +717,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
         for (int b = 0; b < 2; ++b) {
             bar_init(tfull(b), 1);
             bar_init(tempty(b), 2 * kEpiWarps);
-        }
-        for (int i = 0; i < kSlots; ++i) {
-            bar_init(sfull(i), 1);
-            bar_init(sempty(i), 2 * kEpiWarps + 3);  // both CTAs' epilogue and copy warps, the product warp
         }
         bar_init_fence();
 #pragma unroll
@@ -752,50 +737,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
 
-    // the i-th tile of this pair; every warp that asks releases the slot
-    auto next_tile = [&](uint32_t i, Tile* t) {
-        const int s = i % kSlots;
-        const bool ok = bar_wait(sfull(s), (i / kSlots) & 1, &dead);
-        const uint4 lo = lds16(smem_addr(&slot_tile[s])), hi = lds16(smem_addr(&slot_tile[s]) + 16);
-        t->use = lo.x; t->m = lo.y; t->n = lo.z; t->split = lo.w;
-        t->kb0 = hi.x; t->kb1 = hi.y;
-        return ok;
-    };
-    auto release_slot = [&](uint32_t i) { bar_arrive_cluster(cluster_addr(sempty(i % kSlots), 0)); };
+    uint32_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kUses; ++i) total += static_cast<uint32_t>(shapes[i].tiles);
+    const uint32_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
-    if (warp == 10) {
-        // claims and works out tiles a few ahead of the warps that use them: the copies and
-        // the products stand still for as long as their threads think
-        if (rank == 0 && lane == 0) {
-            int64_t total = 0;
-            for (int i = 0; i < kUses; ++i) total += shapes[i].tiles;
-            const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-            for (uint32_t i = 0;; ++i) {
-                const int s = i % kSlots;
-                const int64_t t = i == 0 ? pair : npairs + static_cast<int64_t>(atomicAdd(batch.next, 1));
-                Tile x{};
-                if (t < total) x = tile_at(t, shapes);
-                else x.use = -1;
-                if (!bar_wait(sempty(s), ((i / kSlots) & 1) ^ 1, &dead)) break;
-                for (uint32_t r = 0; r < 2; ++r) {
-                    const uint32_t at = cluster_addr(smem_addr(&slot_tile[s]), r);
-                    const uint32_t bar = cluster_addr(sfull(s), r);
-                    bar_expect_cluster(bar, sizeof(Tile));
-                    store_cluster(at, make_int4(x.use, x.m, x.n, x.split), bar);
-                    store_cluster(at + 16, make_int4(x.kb0, x.kb1, 0, 0), bar);
-                }
-                if (x.use < 0) break;
-            }
-        }
-    } else if (warp == 8) {
+    if (warp == 8) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (uint32_t i = 0; ok; ++i) {
-                Tile x;
-                if (!(ok = next_tile(i, &x))) break;
-                release_slot(i);
-                if (x.use < 0) break;
+            for (uint32_t t = pair; ok && t < total; t += npairs) {
+                const Tile x = tile_at(t, shapes);
                 const int m = x.m * kTile + static_cast<int>(rank) * kHalf, n = x.n * kTile + static_cast<int>(rank) * kHalf;
                 if (x.use == USE_DH) ok = copy_operands<USE_DH>(batch, m, n, x, it, rank, base, bar0, &dead);
                 else if (x.use == USE_DW) ok = copy_operands<USE_DW>(batch, m, n, x, it, rank, base, bar0, &dead);
@@ -810,14 +762,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
         if (rank == 0 && lane == 0) {
             uint32_t it = 0, j = 0;
             bool ok = true;
-            for (uint32_t i = 0; ok; ++i) {
-                Tile x;
-                if (!(ok = next_tile(i, &x))) break;
-                release_slot(i);
-                if (x.use < 0) break;
+            for (uint32_t t = pair; ok && t < total; t += npairs) {
+                const Tile x = tile_at(t, shapes);
                 if (x.kb0 == x.kb1) continue;
                 const int b = j & 1;
-                if (!(ok = bar_wait(tempty(b), ((j >> 1) & 1) ^ 1, &dead))) break;
+                if (!(ok = bar_wait<true>(tempty(b), ((j >> 1) & 1) ^ 1, &dead))) break;
                 tmem_fence_after();
                 const uint32_t d = tmem + b * kTile;
                 const int blocks = x.kb1 - x.kb0;
@@ -833,11 +782,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t staging = base + kStages * kStageBytes + warp * kStagingBytes;
         uint32_t j = 0;
-        for (uint32_t i = 0;; ++i) {
-            Tile x;
-            if (!__all_sync(0xffffffffu, next_tile(i, &x))) break;
-            if (lane == 0) release_slot(i);
-            if (x.use < 0) break;
+        for (uint32_t t = pair; t < total; t += npairs) {
+            const Tile x = tile_at(t, shapes);
             const bool none = x.kb0 == x.kb1;
             const int b = j & 1;
             if (!none) {
@@ -868,6 +814,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1) 
         }
         __syncthreads();
     }
+    // Arrivals on the other CTA's barriers that nobody waits for have landed before either CTA
+    // leaves: its shared memory is another kernel's then.
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
     tmem_fence_before();
     cluster_sync();
     tmem_fence_after();
@@ -977,9 +926,10 @@ template <int DT> cudaError_t launch_products(const Batch& batch, cudaStream_t s
         if (i == USE_DH && p.M) tiles += kSplitTiles;  // fewer rows on the device may mean more splits
     }
     cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
-    // the cluster's size is the kernel's own; it may start while the kernel before it ends
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    // (the cluster's size is the kernel's own.)  Neither this kernel nor the one after it is
+    // launched to start while the kernel before it ends: that gained nothing here (470 and 471
+    // us), and no CTA then takes over shared memory whose last owner's pair still runs.
+    cfg.numAttrs = 0;
     return cudaLaunchKernelEx(&cfg, product_kernel<DT>, batch);
 }
 
@@ -1305,8 +1255,6 @@ cudaError_t launch_prep(PrepArgs& a, const Call& c, const Space& sp, char* w, in
     a.out = reinterpret_cast<uint16_t*>(w + sp.hidden);
     a.status = status;
     a.vec = c.D % 8 == 0 && c.hs % 8 == 0 && aligned16(c.hidden) && (!a.gh || (aligned16(a.gh) && a.ghs % 8 == 0));
-    a.next = reinterpret_cast<int32_t*>(w + sp.next);
-    a.nnext = static_cast<int32_t>(sp.pieces + 1);
     cudaError_t e = launch_chained(prep_kernel, dim3(static_cast<unsigned>((c.T + a.slab - 1) / a.slab)), kPrepThreads, 0, s, a);
     if (e != cudaSuccess) return e;
     *weight = c.weight;
@@ -1339,7 +1287,6 @@ template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* 
     if (e != cudaSuccess) return e;
     Batch batch{};
     batch.count = a.count;
-    batch.next = a.next;
     batch.status = status;
     Product p{};
     p.M = c.T; p.N = c.V; p.K = c.D;
@@ -1350,8 +1297,8 @@ template <int DT> cudaError_t run_forward(const Call& c, const Space& sp, char* 
     if (!set_product<DT, USE_STATS>(batch, p, a.out, sp.dpad, weight, ws)) return cudaErrorInvalidValue;
     e = launch_products<DT>(batch, s);
     if (e != cudaSuccess) return e;
-    return launch_chained(combine_kernel<DT>, dim3(static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows)), 32 * kJoinRows, 0, s,
-                          static_cast<const int32_t*>(a.count), static_cast<const int32_t*>(a.rows),
+    return launch_plain(combine_kernel<DT>, dim3(static_cast<unsigned>((c.T + kJoinRows - 1) / kJoinRows)), 32 * kJoinRows, s,
+                        static_cast<const int32_t*>(a.count), static_cast<const int32_t*>(a.rows),
                           static_cast<const float2*>(p.part), sp.tpad, static_cast<int>(sp.ntiles),
                           static_cast<const float*>(p.ztarget), static_cast<const void*>(a.out), sp.dpad, weight, ws, c.D,
                           static_cast<const int32_t*>(a.target), loss, lse);
@@ -1379,7 +1326,6 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
     for (int64_t i = 0; i <= sp.pieces; ++i) {
         Batch batch{};
         batch.count = a.count;
-        batch.next = a.next + i;
         batch.status = status;
         for (int64_t piece = i - 1; piece <= i; ++piece) {
             if (piece < 0 || piece >= sp.pieces) continue;
@@ -1423,8 +1369,8 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
         e = launch_products<DT>(batch, s);
         if (e == cudaSuccess && gh && i == sp.pieces) {
             const int64_t quads = c.T * (sp.dpad / 4);
-            e = launch_chained(finish_kernel<DT>, dim3(static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 4 * ddp::device_sm_count()))),
-                               256, 0, s, batch.job[USE_DH], static_cast<const int32_t*>(a.count));
+            e = launch_plain(finish_kernel<DT>, dim3(static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 4 * ddp::device_sm_count()))),
+                             256, s, batch.job[USE_DH], static_cast<const int32_t*>(a.count));
         }
         if (e != cudaSuccess) return e;
     }

@@ -595,3 +595,20 @@ def test_loss_on_another_stream():
     got = f.backward(h, w, y, e2, gl, stream=s)
     s.synchronize()
     assert torch.equal(loss, l2) and torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_loss_many_calls_in_a_row():
+    """Calls of mixed tiles (few rows: the hidden states' gradient is split along the vocabulary) without a pause:
+    no wait may run out, and every call gives the same bits."""
+    T, V, dim = 864, 20000, 1086
+    h, w, y, _ = loss_case(70, T, V, dim, 0.0, BF16)
+    f = lm.VocabLoss(V, dim, BF16)
+    loss, lse = f.forward(h, w, y)
+    gl = torch.full((1,), 1.0 / T, device=DEV)
+    gh, gw = f.backward(h, w, y, lse, gl)
+    for _ in range(300):
+        l2, e2 = f.forward(h, w, y)
+        gh2, gw2 = f.backward(h, w, y, e2, gl)
+    torch.cuda.synchronize()
+    assert D.ddp_lm_status() == 0
+    assert torch.equal(loss, l2) and torch.equal(gh, gh2) and torch.equal(gw, gw2)
