@@ -15,9 +15,8 @@
 //
 // Bound by the tensor cores: 2 T V D operations forward, 8 T V D for a step (6 without the
 // second z).  Measured on a GB300 (2 T V D = 632 GFLOP at 8192 tokens x 50257 words x 768,
-// bf16): z and its statistics 343 us, 1.84 PFLOP/s or 0.96 of the rate cuBLAS reaches
-// here; a step 1.72 ms.  At 4096 x 131072 x 4096 the step, seconds long, runs at what the
-// power limit leaves (1.67 PFLOP/s).
+// bf16): a step 1.72 ms, 1.47 PFLOP/s.  At 4096 x 131072 x 4096 the step, seconds long, runs
+// at what the power limit leaves (1.63 PFLOP/s; cuBLAS for seconds: 1.74).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -33,8 +32,7 @@ constexpr int kPrepThreads = 256;
 constexpr int kFewTokens = 2;      // up to so many the forward pass goes without matrix products
 constexpr int kMaxFewCtas = 1024;
 // Elements of G that are held at a time: 537 MB.  More pieces are more launches, which cost
-// about 8 us each at their ends (8192 x 50257 x 768: 1583 us with half of it, 1565; the masked
-// step at 30522 x 1024: 367 and 340).
+// about 8 us each at their ends (the masked step at 30522 x 1024: 367 us with half of it, 340).
 constexpr int64_t kPieceElements = int64_t{1} << 28;
 constexpr float kLog2e = 1.4426950408889634f;
 
