@@ -74,6 +74,10 @@ class GradClipper:
                the tensors must keep their storage.
     out        tensors receiving the clipped gradients (None: in place).
     norm_type  2 or inf.
+
+    Making one builds the tables of addresses and copies them to the GPU, which waits for
+    the copy: it pays where the gradients keep their storage (main_grad views), once for
+    many steps, and costs about as much as a call where they are made anew each step.
     """
 
     def __init__(self, grads, out=None, norm_type=2.0):
@@ -111,11 +115,25 @@ class GradClipper:
         at = self._tables.data_ptr() + 8 * np.cumsum([0] + [len(p) for p in parts])
         self.offset, self.grads_tab, out_tab, self.dtypes = (int(a) for a in at[:4])
         self.out_tab = None if out is None else out_tab
+        self._streams = {_raw_stream(self.device.index)}   # those on which the allocator knows the memory in use
 
     @classmethod
     def of_reducer(cls, reducer, w=0, norm_type=2.0):
         """Over replica w's reduced gradients: the views of a BucketReducer's main_grad."""
         return cls([reducer.view(p, w) for p in range(reducer.plan.nparams)], norm_type=norm_type)
+
+    def _stream(self):
+        """The current stream's handle.  The tables were allocated on the stream that was current when they
+        were made; on another one the allocator has to learn of their use, or it gives their memory away, while
+        the kernels still read it, when the object and its tensors are dropped."""
+        raw = _raw_stream(self.device.index)
+        if raw not in self._streams:
+            stream = torch.cuda.current_stream(self.device)
+            for t in (self._tables, *self._tensors[0], *(self._tensors[1] or ())):
+                if t is not None:
+                    t.record_stream(stream)
+            self._streams.add(raw)
+        return raw
 
     def norm(self, stream=None):
         """The global norm, as a one-element tensor."""
@@ -125,8 +143,7 @@ class GradClipper:
         norm = torch.empty(1, dtype=torch.float32, device=self.device)
         ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         _check(lib().ddp_grad_norm(self.grads_tab, self.offset, self.dtypes, self.ntensors, self.total, self.norm_type,
-                                   norm.data_ptr(), ws.data_ptr(), DDP_CLIP_WORKSPACE_BYTES,
-                                   _raw_stream(self.device.index)))
+                                   norm.data_ptr(), ws.data_ptr(), DDP_CLIP_WORKSPACE_BYTES, self._stream()))
         return norm
 
     def clip(self, max_norm, stream=None):
@@ -139,7 +156,7 @@ class GradClipper:
         ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         _check(lib().ddp_clip_grads(self.grads_tab, self.out_tab, self.offset, self.dtypes, self.ntensors, self.total,
                                     self.norm_type, max_norm, norm.data_ptr(), ws.data_ptr(),
-                                    DDP_CLIP_WORKSPACE_BYTES, _raw_stream(self.device.index)))
+                                    DDP_CLIP_WORKSPACE_BYTES, self._stream()))
         return norm
 
 

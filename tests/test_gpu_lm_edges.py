@@ -1,0 +1,55 @@
+"""Clipping, embedding and vocabulary loss where memory, streams, ranges of values and
+paths are out of the ordinary: what a dropped object's memory may become, losses whose
+weights differ by many orders of magnitude, shapes that take the rarer branches.
+
+Tolerances are derived as in test_gpu_lm.py (u: a type's unit roundoff), from which the
+helpers come."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from allreduce_ddp_assign_gb300 import lm
+from test_gpu_lm import DEV, NORM_REL, gen, norm64, randn
+
+
+def busy_stream():
+    """A stream with about half a second of waiting queued on it, after the current stream's work."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1_000_000_000)
+    return s
+
+
+def addresses_given_out(like):
+    """Where the allocator puts new tensors of these sizes (nothing is written to them)."""
+    kept = [torch.empty_like(t) for t in like for _ in range(8)]
+    return {t.data_ptr() for t in kept}
+
+
+# ---------------------------------------------------------------------------
+# memory in use on another stream
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("call", ["norm", "clip"])
+def test_a_dropped_clipper_keeps_its_memory_until_the_stream_is_done(call):
+    g = [randn(gen(k), 3001 + k) for k in range(5)]
+    ref = norm64(g, False)
+    out = [torch.empty_like(t) for t in g]
+    c = lm.GradClipper(g, out=out)
+    held = [c._tables] + g + out
+    places, sizes = {t.data_ptr() for t in held}, [torch.empty_like(t, device="meta") for t in held]
+    # first uses and the memory of the new tensors below may wait for the GPU: they come before
+    c.norm(), c.clip(1.0), addresses_given_out([torch.empty_like(t, device=DEV) for t in sizes])
+    s = busy_stream()
+    got = c.clip(0.5 * ref, stream=s) if call == "clip" else c.norm(stream=s)
+    del c, g, out, held
+    new = addresses_given_out([torch.empty_like(t, device=DEV) for t in sizes])
+    waiting = not s.query()
+    assert not places & new
+    assert waiting   # else the check says nothing
+    s.synchronize()
+    assert abs(float(got) - ref) <= NORM_REL * ref
