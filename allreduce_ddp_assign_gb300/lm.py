@@ -81,6 +81,8 @@ class GradClipper:
     """
 
     def __init__(self, grads, out=None, norm_type=2.0):
+        # (lists of its own: the tables below keep pointing at these tensors whatever becomes of the caller's)
+        grads, out = tuple(grads), None if out is None else tuple(out)
         if norm_type not in (2, 2.0, math.inf):
             raise ValueError(f"norm_type {norm_type} is neither 2 nor inf")
         self.norm_type = DDP_NORM_INF if norm_type == math.inf else DDP_NORM_L2

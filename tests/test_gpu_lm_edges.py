@@ -53,3 +53,16 @@ def test_a_dropped_clipper_keeps_its_memory_until_the_stream_is_done(call):
     assert waiting   # else the check says nothing
     s.synchronize()
     assert abs(float(got) - ref) <= NORM_REL * ref
+
+
+def test_a_clipper_holds_its_tensors_whatever_becomes_of_the_lists():
+    g = [randn(gen(9), 5000), None, randn(gen(10), 70)]
+    out = [torch.empty_like(t) if t is not None else None for t in g]
+    ref = norm64(g, False)
+    places = {t.data_ptr() for t in g + out if t is not None}
+    sizes = [torch.empty_like(t) for t in g if t is not None]
+    c = lm.GradClipper(g, out=out)
+    g.clear()
+    out[:] = [None] * 3
+    assert not places & addresses_given_out(sizes)
+    assert abs(float(c.clip(1.0)) - ref) <= NORM_REL * ref
