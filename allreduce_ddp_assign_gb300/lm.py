@@ -5,7 +5,10 @@ Each object keeps what a program keeps from step to step (sizes, pointer tables)
 and forwards to the library, which does all of the work.  Calls run on `stream`
 (default: torch's current stream).  Scratch memory is taken from torch's
 allocator for the length of a call, on the stream that the call runs on, and so
-are outputs that the caller does not pass.
+are outputs that the caller does not pass.  Tensors passed to a call with `stream`
+may be dropped when it returns: the allocator is told of their use there.  (As
+everywhere in torch, `stream` does not wait for the work that fills them, and
+outputs belong to the stream that they were made on.)
 
 The smallest calls take a few microseconds on the GPU, so little is done on the
 way there: attributes are read once, and addresses go to the library as integers.
@@ -59,6 +62,14 @@ def _ids(x, name) -> int:
     if x.dim() != 1 or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector, got shape {tuple(x.shape)}")
     return size
+
+
+def _lend(stream, *tensors) -> None:
+    """Memory of these tensors, allocated on other streams, is in use on this one: it is not
+    given away before the work queued here, whatever becomes of the tensors."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _floats(x, name) -> None:
@@ -130,10 +141,7 @@ class GradClipper:
         the kernels still read it, when the object and its tensors are dropped."""
         raw = _raw_stream(self.device.index)
         if raw not in self._streams:
-            stream = torch.cuda.current_stream(self.device)
-            for t in (self._tables, *self._tensors[0], *(self._tensors[1] or ())):
-                if t is not None:
-                    t.record_stream(stream)
+            _lend(torch.cuda.current_stream(self.device), self._tables, *self._tensors[0], *(self._tensors[1] or ()))
             self._streams.add(raw)
         return raw
 
@@ -176,7 +184,9 @@ class TokenEmbedding:
         """out[t] = scale * weight[ids[t]], a [tokens, dim] tensor."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.forward(weight, ids, out)
+                res = self.forward(weight, ids, out)
+            _lend(stream, weight, ids, out)
+            return res
         n, dim = ids.numel(), self.dim
         id_bytes = _ids(ids, "ids")
         ws = _rows(weight, "weight", self.vocab, dim, self._same)
@@ -193,7 +203,9 @@ class TokenEmbedding:
         grad_weight (of dtype, or float32: a main_grad view)."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.backward(grad_out, ids, grad_weight, accumulate)
+                res = self.backward(grad_out, ids, grad_weight, accumulate)
+            _lend(stream, grad_out, ids, grad_weight)
+            return res
         n, dim = ids.numel(), self.dim
         id_bytes = _ids(ids, "ids")
         gs = _rows(grad_out, "grad_out", n, dim, self._same)
@@ -248,7 +260,9 @@ class VocabLoss:
         """(loss, lse) of each token, float32; both 0 where the target is ignore_index."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.forward(hidden, weight, targets)
+                res = self.forward(hidden, weight, targets)
+            _lend(stream, hidden, weight, targets)
+            return res
         n, id_bytes, hs, ws, at, (size, _) = self._inputs(hidden, weight, targets)
         both = torch.empty((2, n), dtype=torch.float32, device=weight.device)
         scratch = torch.empty(size, dtype=torch.uint8, device=weight.device)
@@ -267,8 +281,10 @@ class VocabLoss:
         main_grad view)."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.backward(hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight, accumulate,
-                                     need_hidden, need_weight)
+                res = self.backward(hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight, accumulate,
+                                    need_hidden, need_weight)
+            _lend(stream, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
+            return res
         n, id_bytes, hs, ws, at, (_, size) = self._inputs(hidden, weight, targets)
         _floats(lse, "lse")
         _floats(grad_loss, "grad_loss")

@@ -13,7 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from allreduce_ddp_assign_gb300 import lm
-from test_gpu_lm import DEV, NORM_REL, gen, norm64, randn
+from test_gpu_lm import BF16, DEV, NORM_REL, gen, norm64, randn
 
 
 def busy_stream():
@@ -25,9 +25,9 @@ def busy_stream():
     return s
 
 
-def addresses_given_out(like):
+def addresses_given_out(like, copies=17):
     """Where the allocator puts new tensors of these sizes (nothing is written to them)."""
-    kept = [torch.empty_like(t) for t in like for _ in range(8)]
+    kept = [torch.empty_like(t) for t in like for _ in range(copies)]
     return {t.data_ptr() for t in kept}
 
 
@@ -42,8 +42,9 @@ def test_a_dropped_clipper_keeps_its_memory_until_the_stream_is_done(call):
     c = lm.GradClipper(g, out=out)
     held = [c._tables] + g + out
     places, sizes = {t.data_ptr() for t in held}, [torch.empty_like(t, device="meta") for t in held]
-    # first uses and the memory of the new tensors below may wait for the GPU: they come before
-    c.norm(), c.clip(1.0), addresses_given_out([torch.empty_like(t, device=DEV) for t in sizes])
+    # first uses and memory for the tensors below may wait for the GPU: they come before, for one copy
+    # less, so that the check has to take a block that was not free before
+    c.norm(), c.clip(1.0), addresses_given_out([torch.empty_like(t, device=DEV) for t in sizes], 16)
     s = busy_stream()
     got = c.clip(0.5 * ref, stream=s) if call == "clip" else c.norm(stream=s)
     del c, g, out, held
@@ -66,3 +67,37 @@ def test_a_clipper_holds_its_tensors_whatever_becomes_of_the_lists():
     out[:] = [None] * 3
     assert not places & addresses_given_out(sizes)
     assert abs(float(c.clip(1.0)) - ref) <= NORM_REL * ref
+
+
+def test_tensors_passed_to_another_stream_may_be_dropped():
+    V, dim, T = 500, 72, 1100
+    held = dict(weight=randn(gen(1), V, dim, dtype=BF16), hidden=randn(gen(2), T, dim, dtype=BF16),
+                ids=torch.randint(0, V, (T,), generator=gen(3), device=DEV), lse=None,
+                gl=torch.rand(T, generator=gen(4), device=DEV))
+    e, f = lm.TokenEmbedding(V, dim, BF16), lm.VocabLoss(V, dim, BF16)
+
+    def calls(h, **on):
+        x = e.forward(h["weight"], h["ids"], **on)
+        gw = e.backward(h["hidden"], h["ids"], **on)
+        loss, lse = f.forward(h["hidden"], h["weight"], h["ids"], **on)
+        gh, gw2 = f.backward(h["hidden"], h["weight"], h["ids"], h["lse"], h["gl"], **on)
+        return x, gw, loss, lse, gh, gw2
+
+    held["lse"] = f.forward(held["hidden"], held["weight"], held["ids"])[1].clone()
+    want = calls(held)
+    places, sizes = {t.data_ptr() for t in held.values()}, [torch.empty_like(t) for t in held.values()]
+    addresses_given_out(sizes, 16)
+    with torch.cuda.stream(warm := torch.cuda.Stream()):   # its scratch memory and outputs
+        warm.wait_stream(torch.cuda.default_stream())
+        calls(held)
+        warm.synchronize()
+    with torch.cuda.stream(warm):
+        torch.cuda._sleep(1_000_000_000)
+    got = calls(held, stream=warm)
+    held.clear()
+    new = addresses_given_out(sizes)
+    waiting = not warm.query()
+    assert not places & new
+    assert waiting   # else the check says nothing
+    warm.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
