@@ -8,7 +8,8 @@ allocator for the length of a call, on the stream that the call runs on, and so
 are outputs that the caller does not pass.  Tensors passed to a call with `stream`
 may be dropped when it returns: the allocator is told of their use there.  (As
 everywhere in torch, `stream` does not wait for the work that fills them, and
-outputs belong to the stream that they were made on.)
+outputs belong to the stream that they were made on.)  Everything lies on the
+current device, where the library launches; other tensors are refused.
 
 The smallest calls take a few microseconds on the GPU, so little is done on the
 way there: attributes are read once, and addresses go to the library as integers.
@@ -29,6 +30,11 @@ except ImportError:  # pragma: no cover - another torch
     def _raw_stream(device):
         return torch.cuda.current_stream(device).cuda_stream
 
+try:
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:  # pragma: no cover - another torch
+    from torch.cuda import current_device as _current_device
+
 _DTYPES = {torch.float32: DDP_F32, torch.bfloat16: DDP_BF16, torch.float16: DDP_F16}
 
 
@@ -39,12 +45,19 @@ def _dtype(t) -> int:
         raise ValueError(f"dtype {t} is not float32, bfloat16 or float16") from None
 
 
+def _here(x, name) -> None:
+    """x lies on the current device, where the library launches."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} is not on the GPU")
+    if x.get_device() != _current_device():
+        raise ValueError(f"{name} is on {x.device}, the current device is cuda:{_current_device()}")
+
+
 def _rows(x, name, rows, dim, dtypes) -> int:
     """x as a [rows, dim] matrix with contiguous rows on the GPU; its row stride."""
     if x.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {x.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} is not on the GPU")
+    _here(x, name)
     if x.dim() == 2:
         r, c = x.shape
         s, one = x.stride()
@@ -59,6 +72,7 @@ def _ids(x, name) -> int:
     size = {torch.int64: 8, torch.int32: 4}.get(x.dtype)
     if size is None or not x.is_cuda:
         raise ValueError(f"{name} must be int32 or int64 on the GPU")
+    _here(x, name)
     if x.dim() != 1 or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector, got shape {tuple(x.shape)}")
     return size
@@ -75,6 +89,7 @@ def _lend(stream, *tensors) -> None:
 def _floats(x, name) -> None:
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor on the GPU")
+    _here(x, name)
 
 
 class GradClipper:
@@ -109,9 +124,12 @@ class GradClipper:
             _dtype(g.dtype)
             if not g.is_cuda or not g.is_contiguous():
                 raise ValueError(f"gradient {k} is not a contiguous tensor on the GPU")
+            _here(g, f"gradient {k}")
             if o is not None and (o.dtype != g.dtype or o.numel() != g.numel() or not o.is_cuda
                                   or not o.is_contiguous()):
                 raise ValueError(f"output {k} is not a contiguous {g.dtype} tensor of {g.numel()} elements on the GPU")
+            if o is not None:
+                _here(o, f"output {k}")
         self.device = given[0].device if given else torch.device("cuda", torch.cuda.current_device())
         self._tensors = (grads, out)   # the pointer tables below point into these
         n = [0 if g is None else g.numel() for g in grads]
@@ -139,6 +157,8 @@ class GradClipper:
         """The current stream's handle.  The tables were allocated on the stream that was current when they
         were made; on another one the allocator has to learn of their use, or it gives their memory away, while
         the kernels still read it, when the object and its tensors are dropped."""
+        if self.device.index != _current_device():
+            raise ValueError(f"the gradients are on {self.device}, the current device is cuda:{_current_device()}")
         raw = _raw_stream(self.device.index)
         if raw not in self._streams:
             _lend(torch.cuda.current_stream(self.device), self._tables, *self._tensors[0], *(self._tensors[1] or ()))
@@ -150,10 +170,11 @@ class GradClipper:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.norm()
+        on = self._stream()
         norm = torch.empty(1, dtype=torch.float32, device=self.device)
         ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         _check(lib().ddp_grad_norm(self.grads_tab, self.offset, self.dtypes, self.ntensors, self.total, self.norm_type,
-                                   norm.data_ptr(), ws.data_ptr(), DDP_CLIP_WORKSPACE_BYTES, self._stream()))
+                                   norm.data_ptr(), ws.data_ptr(), DDP_CLIP_WORKSPACE_BYTES, on))
         return norm
 
     def clip(self, max_norm, stream=None):
@@ -162,11 +183,12 @@ class GradClipper:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.clip(max_norm)
+        on = self._stream()
         norm = torch.empty(1, dtype=torch.float32, device=self.device)
         ws = torch.empty(DDP_CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         _check(lib().ddp_clip_grads(self.grads_tab, self.out_tab, self.offset, self.dtypes, self.ntensors, self.total,
                                     self.norm_type, max_norm, norm.data_ptr(), ws.data_ptr(),
-                                    DDP_CLIP_WORKSPACE_BYTES, self._stream()))
+                                    DDP_CLIP_WORKSPACE_BYTES, on))
         return norm
 
 
