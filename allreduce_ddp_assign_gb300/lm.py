@@ -21,8 +21,8 @@ import math
 import numpy as np
 import torch
 
-from . import (DDP_BF16, DDP_CLIP_WORKSPACE_BYTES, DDP_F16, DDP_F32, DDP_NORM_INF, DDP_NORM_L2, _check, lib,
-               ddp_embedding_workspace, ddp_vocab_loss_workspace)
+from . import (DDP_ALLREDUCE, DDP_BF16, DDP_CLIP_WORKSPACE_BYTES, DDP_F16, DDP_F32, DDP_NORM_INF, DDP_NORM_L2, _check,
+               lib, ddp_embedding_workspace, ddp_vocab_loss_workspace)
 
 try:
     from torch._C import _cuda_getCurrentRawStream as _raw_stream
@@ -150,7 +150,12 @@ class GradClipper:
 
     @classmethod
     def of_reducer(cls, reducer, w=0, norm_type=2.0):
-        """Over replica w's reduced gradients: the views of a BucketReducer's main_grad."""
+        """Over replica w's reduced gradients: the views of an all-reducing BucketReducer's main_grad."""
+        if reducer.mode != DDP_ALLREDUCE:
+            # the rest of its main_grad is not written by the reduction, and a norm over the shard is not the model's
+            raise ValueError("after a reduce-scatter a replica holds only its own shard of the reduced gradients")
+        if reducer.main_grad is None:
+            raise ValueError("the reducer keeps no main_grad")
         return cls([reducer.view(p, w) for p in range(reducer.plan.nparams)], norm_type=norm_type)
 
     def _stream(self):

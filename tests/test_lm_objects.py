@@ -1,9 +1,10 @@
-"""What the language-model objects refuse about where tensors lie, with stand-ins for
-tensors on two GPUs (CPU only: no call here reaches a kernel)."""
+"""What the language-model objects refuse about where tensors lie and whose they are, with
+stand-ins for tensors on two GPUs (CPU only: no call here reaches a kernel)."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
+import allreduce_ddp_assign_gb300 as D
 from allreduce_ddp_assign_gb300 import lm
 
 BF16, F32, I64 = torch.bfloat16, torch.float32, torch.int64
@@ -106,3 +107,22 @@ def test_a_clipper_is_refused_where_another_gpu_is_current(two_gpus, call):
     with pytest.raises(ValueError, match="gradients are on cuda:1, the current device is cuda:0"):
         call(c)
     assert not two_gpus.calls
+
+
+class Reducer:
+    """Two parameters' views of a main_grad."""
+
+    def __init__(self, mode, main_grad=()):
+        self.mode, self.main_grad = mode, main_grad
+        self.plan = type("Plan", (), {"nparams": 2})
+
+    def view(self, p, w):
+        return OnGpu((5 + p,), F32, 0)
+
+
+def test_clipping_after_a_reduce_scatter_is_refused(two_gpus):
+    """A replica's main_grad holds reduced values in its own shard only."""
+    with pytest.raises(ValueError, match="its own shard"):
+        lm.GradClipper.of_reducer(Reducer(D.DDP_REDUCE_SCATTER))
+    with pytest.raises(ValueError, match="no main_grad"):
+        lm.GradClipper.of_reducer(Reducer(D.DDP_ALLREDUCE, None))
