@@ -81,6 +81,8 @@ lookup_kernel(const void* weight, int64_t ws, int64_t vocab, int64_t dim, const 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr uint16_t kNone = 0xffff;
+// Tokens are counted in 32 bits, up to a step of the loops beyond the last one (512, and 2048 in the stretches' lengths).
+constexpr int64_t kMaxSortTokens = (int64_t{1} << 31) - 4096;
 constexpr int kMaxRange = 1024;  // ids a sorting CTA owns at most (its counters: 4 bytes an id and warp)
 constexpr int kMinSortCtas = 128;  // a power of two, one wave
 constexpr int kIdBatch = 8;      // loads of ids a thread keeps in flight
@@ -630,7 +632,7 @@ extern "C" ddp_status ddp_embedding_workspace(int64_t ntokens, int64_t vocab, in
 {
     const char* fn = "ddp_embedding_workspace";
     if (!bytes) return ddp::fail(DDP_E_INVAL, "%s: bytes is NULL", fn);
-    if (ntokens < 0 || ntokens >= (int64_t{1} << 31) || vocab < 1 || vocab >= (int64_t{1} << 31) || dim < 1 || dim >= (int64_t{1} << 28))
+    if (ntokens < 0 || ntokens >= kMaxSortTokens || vocab < 1 || vocab >= (int64_t{1} << 31) || dim < 1 || dim >= (int64_t{1} << 28))
         return ddp::fail(DDP_E_INVAL, "%s: ntokens = %lld, vocab = %lld, dim = %lld out of range", fn,
                          static_cast<long long>(ntokens), static_cast<long long>(vocab), static_cast<long long>(dim));
     *bytes = space_for(ntokens, vocab, dim).total;
@@ -647,6 +649,7 @@ extern "C" ddp_status ddp_embedding_backward(const void* grad_out, int64_t grad_
     const char* fn = "ddp_embedding_backward";
     const ddp_status st = check_common(fn, ntokens, vocab, dim, dtype, id_bytes, ids, grad_out, grad_stride, "grad_out");
     if (st != DDP_OK) return st;
+    if (ntokens >= kMaxSortTokens) return fail(DDP_E_INVAL, "%s: ntokens = %lld is 2^31 - 4096 or more", fn, static_cast<long long>(ntokens));
     if (!grad_weight) return fail(DDP_E_INVAL, "%s: grad_weight is NULL", fn);
     if (gw_stride < dim)
         return fail(DDP_E_INVAL, "%s: grad_weight's stride %lld < dim = %lld", fn, static_cast<long long>(gw_stride),

@@ -29,6 +29,9 @@ namespace {
 
 constexpr int kRowTile = 256;   // rows of the gathered arrays are padded to this
 constexpr int kPrepThreads = 256;
+// Tokens are counted in 32 bits, up to a step of the gather's loop (2048) beyond the last one; words up to a tile's.
+constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 4096;
+constexpr int64_t kMaxVocab = (int64_t{1} << 31) - 512;
 constexpr int kFewTokens = 2;      // up to so many the forward pass goes without matrix products
 constexpr int kMaxFewCtas = 1024;
 // Elements of G that are held at a time: 537 MB.  More pieces are more launches, which cost
@@ -271,9 +274,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
     }
     // rows up to the tile's end are zeros (past the T-th the copies supply them): they are terms of dW's sums
     const int end = min(a.T, (all + kRowTile - 1) / kRowTile * kRowTile);
-    for (int r = all + blockIdx.x; r < end; r += gridDim.x)
+    for (int64_t r = static_cast<int64_t>(all) + blockIdx.x; r < end; r += gridDim.x)
         for (int64_t c = tid * 8; c < a.dpad; c += kPrepThreads * 8)
-            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(r) * a.dpad + c) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(a.out + r * a.dpad + c) = make_uint4(0, 0, 0, 0);
 }
 
 // An aligned copy of rows that start anywhere: a thread gathers 8 values at a time, the
@@ -1195,8 +1198,8 @@ ddp_status check(const char* fn, const Call& c, const void* workspace, int64_t w
 {
     using ddp::fail;
     if (c.T < 0) return fail(DDP_E_INVAL, "%s: ntokens = %lld < 0", fn, static_cast<long long>(c.T));
-    if (c.T >= (int64_t{1} << 31) - 512) return fail(DDP_E_INVAL, "%s: ntokens = %lld is too large", fn, static_cast<long long>(c.T));
-    if (c.V < 1 || c.V >= (int64_t{1} << 31) - 512) return fail(DDP_E_INVAL, "%s: vocab = %lld out of range", fn, static_cast<long long>(c.V));
+    if (c.T >= kMaxTokens) return fail(DDP_E_INVAL, "%s: ntokens = %lld is too large", fn, static_cast<long long>(c.T));
+    if (c.V < 1 || c.V >= kMaxVocab) return fail(DDP_E_INVAL, "%s: vocab = %lld out of range", fn, static_cast<long long>(c.V));
     if (c.D < 1 || c.D >= (int64_t{1} << 24)) return fail(DDP_E_INVAL, "%s: dim = %lld out of range", fn, static_cast<long long>(c.D));
     if (c.dtype != DDP_BF16 && c.dtype != DDP_F16) return fail(DDP_E_INVAL, "%s: dtype %d is neither DDP_BF16 nor DDP_F16", fn, c.dtype);
     if (c.id_bytes != 4 && c.id_bytes != 8) return fail(DDP_E_INVAL, "%s: id_bytes = %d is neither 4 nor 8", fn, c.id_bytes);
@@ -1385,7 +1388,7 @@ extern "C" ddp_status ddp_vocab_loss_workspace(int64_t ntokens, int64_t vocab, i
 {
     const char* fn = "ddp_vocab_loss_workspace";
     if (!forward_bytes || !backward_bytes) return ddp::fail(DDP_E_INVAL, "%s: an output is NULL", fn);
-    if (ntokens < 0 || ntokens >= (int64_t{1} << 31) - 512 || vocab < 1 || vocab >= (int64_t{1} << 31) - 512 || dim < 1 ||
+    if (ntokens < 0 || ntokens >= kMaxTokens || vocab < 1 || vocab >= kMaxVocab || dim < 1 ||
         dim >= (int64_t{1} << 24) || piece < 0)
         return ddp::fail(DDP_E_INVAL, "%s: ntokens = %lld, vocab = %lld, dim = %lld, piece = %lld out of range", fn,
                          static_cast<long long>(ntokens), static_cast<long long>(vocab), static_cast<long long>(dim),

@@ -954,6 +954,7 @@ ddp_status ddp_embedding_workspace(int64_t ntokens, int64_t vocab, int64_t dim, 
  *   grad_out     DEVICE dtype [ntokens x dim], rows grad_stride apart.
  *   grad_weight  DEVICE gw_dtype [vocab x dim], rows gw_stride apart; gw_dtype is
  *                dtype or DDP_F32 (a main_grad segment).
+ * ntokens < 2^31 - 4096.
  * Errors: as ddp_embedding_forward; DDP_E_INVAL for another gw_dtype or too
  * small a workspace.
  */
@@ -985,7 +986,7 @@ ddp_status ddp_vocab_loss_workspace(int64_t ntokens, int64_t vocab, int64_t dim,
  *   weight   DEVICE dtype [vocab x dim], rows weight_stride apart.
  *   loss, lse  DEVICE float[ntokens].
  * dtype is DDP_BF16 or DDP_F16; products are exact and summed in fp32.
- * ntokens and vocab < 2^31 - 512, dim < 2^24.
+ * ntokens < 2^31 - 4096, vocab < 2^31 - 512, dim < 2^24.
  * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, a stride below dim,
  * another dtype, id_bytes, a NULL pointer with ntokens > 0, too small a
  * workspace); DDP_E_CUDA.

@@ -150,3 +150,16 @@ def test_objects_refuse_on_the_host():
         e.forward(cpu, torch.zeros(3))
     with pytest.raises(ValueError, match="bfloat16 or float16"):
         lm.VocabLoss(10, 8, torch.float32)
+
+
+def test_token_counts_whose_loops_would_leave_32_bits():
+    """The kernels step through the tokens in 32 bits, beyond the last one by up to a step."""
+    for n in ((1 << 31) - 4096, (1 << 31) - 2048, (1 << 31) - 600, (1 << 31) - 1):
+        refused("ntokens", D.ddp_embedding_backward, BWD, ntokens=n)
+        refused("ntokens", D.ddp_vocab_loss_forward, LOSS, ntokens=n)
+        refused("ntokens", D.ddp_vocab_loss_backward, GRAD, ntokens=n)
+        for sizes in (D.ddp_embedding_workspace, D.ddp_vocab_loss_workspace):
+            with pytest.raises(D.DdpError, match="ntokens"):
+                sizes(n, 100, 64)
+    assert D.ddp_embedding_workspace((1 << 31) - 4097, 100, 64) > 8 << 31
+    assert D.ddp_vocab_loss_workspace((1 << 31) - 4097, 100, 64)[0] > 2 * 64 << 31
