@@ -44,6 +44,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // numbers.  bf16 has fp32's exponents and needs none.
 template <int DT> constexpr float g_scale() { return DT == DDP_F16 ? 16384.f : 1.f; }
 
+// A token whose |grad_loss| is below kMinRatio of the largest would leave too few of fp16's
+// bits to its probabilities.  Its row of G is held times 2^k, back up to kMinRatio or just
+// above (probabilities down to 2^-18 normal, the smallest step 2^-28); dH's row is multiplied by
+// 2^-k in fp32, and dW takes its hidden state times 2^-k in fp16, exactly but for what
+// falls below fp16's smallest normal number.  Other rows are not touched by this (k = 0).
+constexpr float kMinRatio = 0x1p-10f;
+
 // dH's tiles are split along the vocabulary while there are fewer than this many
 // of them, about one for each pair of SMs (by a constant, so that the order of its sums
 // does not depend on the device).
@@ -55,7 +62,7 @@ __host__ __device__ __forceinline__ int dh_splits(int mt, int nt, int nkb)
 }
 
 struct Space {
-    int64_t count, gmax, rows, target, ratio, lse, hidden, part, ztarget, grad, acc, weight, total;
+    int64_t count, gmax, rows, target, ratio, back, lse, hidden, hidden_w, part, ztarget, grad, acc, weight, total;
     int64_t piece, pieces, ntiles, tpad, dpad, grad_bytes;
 };
 
@@ -88,6 +95,9 @@ Space space_for(bool backward, int64_t T, int64_t V, int64_t D, int64_t piece, b
     s.hidden = take(2 * s.tpad * s.dpad);
     if (backward) {
         s.ratio = take(4 * s.tpad);
+        // (fp16's; bf16 has no use for these two)
+        s.back = take(4 * s.tpad);
+        s.hidden_w = take(2 * s.tpad * s.dpad);
         s.lse = take(4 * s.tpad);
         s.grad_bytes = round_up(2 * s.tpad * most, 256);
         s.grad = take(s.grad_bytes * std::min<int64_t>(s.pieces, 2));
@@ -129,7 +139,9 @@ struct PrepArgs {
     const float* gl;
     int32_t gl_stride;
     float* lse;           // gathered
-    float* ratio;         // gathered: grad_loss / gmax * g_scale
+    float* ratio;         // gathered: grad_loss / gmax * g_scale (fp16: and * 2^k)
+    float* back;          // fp16, gathered: 2^-k
+    uint16_t* out_w;      // fp16, [tpad][dpad]: gathered rows times 2^-k (nullptr: no weight gradient)
     float* gmax;          // largest finite |grad_loss| of the gathered rows (1 if that is 0)
     uint16_t* gh;         // rows to clear
     int64_t ghs;
@@ -168,6 +180,15 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t d
     return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
+// eight fp16 values times f
+__device__ __forceinline__ uint4 times8(uint4 v, float f)
+{
+    __half* h = reinterpret_cast<__half*>(&v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(__half2float(h[j]) * f);
+    return v;
+}
+
 // Every CTA counts the tokens with a target before its own slab, and all of them, itself:
 // no launch of its own for the places, and 8 bytes a token and CTA from L2.  Bound by the
 // latency of four dependent reads; 13 us for 8192 rows of 768 (25 MB) with cold caches.
@@ -176,6 +197,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
     __shared__ int sh[kPrepThreads / 32];
     __shared__ float shf[kPrepThreads / 32];
     __shared__ int place[kPrepThreads];  // of the slab's tokens: gathered row or -1
+    __shared__ float backs[kPrepThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = blockIdx.x * a.slab, t1 = min(a.T, t0 + a.slab);
     wait_for_previous();
@@ -227,7 +249,18 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
             a.target[at] = static_cast<int32_t>(y);
             if (a.gl) {
                 a.lse[at] = a.lse_in[t];
-                a.ratio[at] = a.gl[static_cast<int64_t>(t) * a.gl_stride] / gm * a.g_scale;
+                float r = a.gl[static_cast<int64_t>(t) * a.gl_stride] / gm, back = 1.f;
+                if (a.back) {
+                    const float size = fabsf(r);
+                    if (size > 0.f && size < kMinRatio) {
+                        const int k = ilogbf(kMinRatio) - ilogbf(size);
+                        r = ldexpf(r, k);
+                        back = ldexpf(1.f, -k);
+                    }
+                    a.back[at] = back;
+                }
+                backs[tid] = back;
+                a.ratio[at] = r * a.g_scale;
             }
         } else if (t < t1 && a.loss) {
             a.loss[t] = 0.f;
@@ -240,43 +273,51 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(PrepArgs a)
     const int rows = t1 - t0;
     for (int64_t i = tid; i < vecs * rows; i += 4 * kPrepThreads) {
         uint4 v[4];
-        uint16_t* to[4];
+        uint16_t *to[4], *to_w[4];
+        float back[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t k = i + j * kPrepThreads;
-            to[j] = nullptr;
+            to[j] = to_w[j] = nullptr;
             if (k >= vecs * rows) continue;
             const int r = static_cast<int>(static_cast<uint32_t>(k) / static_cast<uint32_t>(vecs));
             const int64_t c = (k - r * vecs) * 8;
             v[j] = make_uint4(0, 0, 0, 0);
             if (place[r] >= 0) {
                 to[j] = a.out + static_cast<int64_t>(place[r]) * a.dpad + c;
+                if (a.out_w) to_w[j] = a.out_w + static_cast<int64_t>(place[r]) * a.dpad + c, back[j] = backs[r];
                 v[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs + c);
             } else if (a.gh) {
                 to[j] = a.gh + static_cast<int64_t>(t0 + r) * a.ghs + c;
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
             if (to[j]) *reinterpret_cast<uint4*>(to[j]) = v[j];
+            if (to_w[j]) *reinterpret_cast<uint4*>(to_w[j]) = back[j] == 1.f ? v[j] : times8(v[j], back[j]);
+        }
     }
     if (!a.vec) {
         const int64_t all_vecs = a.dpad / 8;
         for (int64_t i = tid; i < all_vecs * rows; i += kPrepThreads) {
             const int r = static_cast<int>(i / all_vecs);
             const int64_t c = (i - r * all_vecs) * 8;
-            if (place[r] >= 0)
-                *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(place[r]) * a.dpad + c) =
-                    load8(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs, c, a.dim);
-            else if (a.gh)
+            if (place[r] >= 0) {
+                const uint4 v = load8(static_cast<const uint16_t*>(a.hidden) + static_cast<int64_t>(t0 + r) * a.hs, c, a.dim);
+                const int64_t at = static_cast<int64_t>(place[r]) * a.dpad + c;
+                *reinterpret_cast<uint4*>(a.out + at) = v;
+                if (a.out_w) *reinterpret_cast<uint4*>(a.out_w + at) = backs[r] == 1.f ? v : times8(v, backs[r]);
+            } else if (a.gh)
                 for (int64_t k = c; k < min(c + 8, a.dim); ++k) a.gh[static_cast<int64_t>(t0 + r) * a.ghs + k] = 0;
         }
     }
     // rows up to the tile's end are zeros (past the T-th the copies supply them): they are terms of dW's sums
     const int end = min(a.T, (all + kRowTile - 1) / kRowTile * kRowTile);
     for (int64_t r = static_cast<int64_t>(all) + blockIdx.x; r < end; r += gridDim.x)
-        for (int64_t c = tid * 8; c < a.dpad; c += kPrepThreads * 8)
+        for (int64_t c = tid * 8; c < a.dpad; c += kPrepThreads * 8) {
             *reinterpret_cast<uint4*>(a.out + r * a.dpad + c) = make_uint4(0, 0, 0, 0);
+            if (a.out_w) *reinterpret_cast<uint4*>(a.out_w + r * a.dpad + c) = make_uint4(0, 0, 0, 0);
+        }
 }
 
 // An aligned copy of rows that start anywhere: a thread gathers 8 values at a time, the
@@ -356,6 +397,7 @@ struct Product {
     // DH, DW
     const float* gmax;
     float inv_scale;
+    const float* back;    // DH, fp16: a factor for each row
     float* acc;           // dH: fp32 sums over pieces and splits, [split][row][ald]
     int64_t ald;
     int32_t first, last;
@@ -568,6 +610,8 @@ __device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, c
         const bool adds = sums ? !p.first : USE == USE_DW && p.accumulate;
         const bool f32 = USE == USE_DW && p.out_f32;
         const int32_t token = USE == USE_DH && result && m < M ? p.rows[m] : 0;
+        constexpr bool kRowFactors = USE == USE_DH && DT == DDP_F16;
+        const float row_alpha = kRowFactors && result && m < M ? alpha * p.back[m] : alpha;
         for (int q = 0; q < 4; ++q) {
             const int64_t n = n0 + q * 32 + (lane & 7) * 4;
             if (n0 + q * 32 >= p.N) break;
@@ -610,6 +654,7 @@ __device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, c
             for (int i = 0; i < 8; ++i) {
                 const int r = i * 4 + (lane >> 3);
                 const int32_t to = USE == USE_DH ? __shfl_sync(0xffffffffu, token, r) : 0;
+                const float factor = kRowFactors ? __shfl_sync(0xffffffffu, row_alpha, r) : alpha;
                 const uint4 raw = lds16(staged(staging, r, lane & 7));
                 float x[4] = {__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), __uint_as_float(raw.w)};
                 const int64_t row = m0 + r;
@@ -623,7 +668,7 @@ __device__ __forceinline__ void epilogue(const Product& p, const Shape& shape, c
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = x[j] * alpha + (USE == USE_DW ? old[i][j] : 0.f);
+                for (int j = 0; j < 4; ++j) x[j] = x[j] * factor + (USE == USE_DW ? old[i][j] : 0.f);
                 const int64_t at = (USE == USE_DH ? to : p.v0 + row) * p.os + n;
                 if (f32) {
                     float* o = static_cast<float*>(p.out) + at;
@@ -833,10 +878,11 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Pro
     wait_for_previous();
     const Shape sh = shape_of(p, USE_DH, *count);
     if (sh.splits == 1) return;
-    const float alpha = *p.gmax * p.inv_scale;
+    const float scale = *p.gmax * p.inv_scale;
     const int64_t quads = p.ald / 4, size = static_cast<int64_t>(sh.mt) * kTile * p.ald;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < sh.M * quads; i += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t row = i / quads, n = (i - row * quads) * 4;
+        const float alpha = DT == DDP_F16 ? scale * p.back[row] : scale;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int s = 0; s < sh.splits; ++s) {
@@ -1319,6 +1365,10 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
     a.gh = static_cast<uint16_t*>(gh);
     a.ghs = ghs;
     a.g_scale = g_scale<DT>();
+    if (DT == DDP_F16) {
+        a.back = reinterpret_cast<float*>(w + sp.back);
+        if (gw) a.out_w = reinterpret_cast<uint16_t*>(w + sp.hidden_w);
+    }
     const void* weight;
     int64_t ws;
     cudaError_t e = launch_prep(a, c, sp, w, status, s, &weight, &ws);
@@ -1341,6 +1391,7 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
             p.g = w + sp.grad + (piece & 1) * sp.grad_bytes;
             p.gld = sp.piece;
             p.gmax = a.gmax;
+            p.back = a.back;
             p.inv_scale = 1.f / g_scale<DT>();
             p.rows = a.rows;
             p.acc = reinterpret_cast<float*>(w + sp.acc);
@@ -1364,7 +1415,7 @@ cudaError_t run_backward(const Call& c, const Space& sp, char* w, int* status, c
                 q.M = words; q.N = c.D; q.K = c.T;
                 q.out = gw; q.os = gws; q.out_f32 = gw_f32; q.accumulate = accumulate;
                 q.vec = aligned16(gw) && gws % 4 == 0;
-                if (!set_product<DT, USE_DW>(batch, q, p.g, p.gld, a.out, sp.dpad)) return cudaErrorInvalidValue;
+                if (!set_product<DT, USE_DW>(batch, q, p.g, p.gld, DT == DDP_F16 ? a.out_w : a.out, sp.dpad)) return cudaErrorInvalidValue;
             }
         }
         e = launch_products<DT>(batch, s);

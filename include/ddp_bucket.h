@@ -1000,9 +1000,14 @@ ddp_status ddp_vocab_loss_forward(const void* hidden, int64_t hidden_stride, con
  * ddp_vocab_loss_backward -- gradients of sum_t grad_loss[t] * loss[t]:
  *   G[t][v] = grad_loss[t] * (exp(z[t][v] - lse[t]) - [v == targets[t]])
  *   grad_hidden = G x weight,   grad_weight (= | +=) G^T x hidden
- * with z computed again and G held for one piece of the vocabulary at a time, in
- * `dtype` after division by the largest |grad_loss| (exactly that factor is
- * put back in fp32).  Ignored tokens get rows of zeros in grad_hidden.
+ * with z computed again and G held for one piece of the vocabulary at a time,
+ * rounded to `dtype` after division by the largest finite |grad_loss| (that factor is
+ * put back in fp32): a gradient is about 1.2 times as far from the exact one as a
+ * single rounding of it would be.  DDP_F16: a token's own |grad_loss| counts instead
+ * below 2^-10 of the largest, so that grad_hidden's rows are right at any ratio; for
+ * grad_weight its hidden state is held times that ratio (over 2^-10) in fp16, where
+ * a state of size 1 loses bits below 2^-24 of the largest, and adds nothing below
+ * 2^-35.  Ignored tokens get rows of zeros in grad_hidden.
  *   lse          what ddp_vocab_loss_forward wrote.
  *   grad_loss    DEVICE float, element t at grad_loss[t * grad_loss_stride];
  *                grad_loss_stride is 1, or 0 for one value for every token.

@@ -13,7 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from allreduce_ddp_assign_gb300 import lm
-from test_gpu_lm import BF16, DEV, NORM_REL, gen, norm64, randn
+from test_gpu_lm import BF16, DEV, F16, F32, NORM_REL, TINY, U, gen, loss64, loss_case, norm64, randn, within
 
 
 def busy_stream():
@@ -101,3 +101,55 @@ def test_tensors_passed_to_another_stream_may_be_dropped():
     assert waiting   # else the check says nothing
     warm.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# ---------------------------------------------------------------------------
+# losses whose weights differ by many orders of magnitude
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("T,piece,largest", [(90, 0, 1.0), (90, 512, 65536.0), (700, 0, 1024.0)])
+def test_loss_gradients_of_tokens_with_very_different_weights(dt, aligned, T, piece, largest):
+    """Every token's row of grad_hidden is right beside its own grad_loss, however small that is beside the others'.
+
+    G' = (p - onehot) r 2^14 in fp16, r the token's grad_loss over the largest, or between 2^-10 and 2^-9 where that is
+    smaller: off by one rounding (u) or half of the smallest step, 2^-25 / (r 2^14), at most 2^-29 of the token's own
+    grad_loss where r was moved and 2^-39 of the largest elsewhere.  Where r was moved by 2^k the weight's gradient
+    takes the hidden state times 2^-k: off by half of the smallest step, 2^-25 2^k."""
+    V, dim = 3000, 64
+    h, w, y, valid = loss_case(80, T, V, dim, 0.1, dt, aligned)
+    size = 10.0 ** -(2.25 * (torch.arange(T, device=DEV) % 5).double())   # 1 to 1e-9
+    gl = ((torch.rand(T, generator=gen(81), device=DEV).double() + 0.25) * size * largest).float()
+    f = lm.VocabLoss(V, dim, dt, piece=piece)
+    _, lse = f.forward(h, w, y)
+    gw = torch.empty(V, dim, dtype=F32, device=DEV)
+    gh, _ = f.backward(h, w, y, lse, gl, grad_weight=gw)
+    r = loss64(h, w, y, valid, gl)
+    g, gv = r["g"], gl.double()[valid][:, None]
+    gmax = float(gv.max())
+    K = max(T, V)
+    eg = r["dg"] + (U[dt] + 4 * 2.0 ** -24 + (K + 2) * 2.0 ** -23) * g.abs()
+    moved = gv / gmax < 2.0 ** -10
+    back = torch.zeros_like(gv)
+    if dt == F16:
+        eg = eg + torch.where(moved, gv * 2.0 ** -29, torch.full_like(gv, gmax * 2.0 ** -39))
+        k = -10 - torch.floor(torch.log2(gv / gmax))
+        back = torch.where(moved, 2.0 ** (k - 25), back)
+    else:
+        eg = eg + 2.0 ** -133
+    want = g @ r["W"]
+    tol = eg @ r["W"].abs() + want.abs() * (U[dt] + 2.0 ** -23) + TINY[dt]
+    got, top = gh[valid].double(), (65504.0 if dt == F16 else 3e38)
+    fits = want.abs() + tol < top
+    within(got[fits], want[fits], tol[fits], "grad_hidden")
+    over = want.abs() - tol > 65520.0 if dt == F16 else ~fits
+    assert bool((got[over].abs() == float("inf")).all())
+    want = g.t() @ r["H"]
+    tol = eg.t() @ r["H"].abs() + (g.abs().t() @ back.expand(-1, dim)) + want.abs() * 2.0 ** -23
+    within(gw, want, tol, "grad_weight")
+    # the rows of small weights are more than their target's term: the check above sees what the others add
+    if dt == F16 and largest > 1:
+        one = -gv * r["W"][y[valid]]
+        small = (gv / gmax < 1e-5)[:, 0]
+        e = (got - one).norm(dim=1)[small] / one.norm(dim=1)[small]
+        assert float(e.median()) > 0.05
