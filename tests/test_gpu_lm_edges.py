@@ -12,8 +12,11 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("no CUDA device", allow_module_level=True)
 
+import allreduce_ddp_assign_gb300 as D
 from allreduce_ddp_assign_gb300 import lm
-from test_gpu_lm import BF16, DEV, F16, F32, NORM_REL, TINY, U, gen, loss64, loss_case, norm64, randn, within
+from allreduce_ddp_assign_gb300.session import BucketReducer
+from test_gpu_lm import (BF16, DEV, F16, F32, NORM_REL, TINY, U, embed_grad64, gen, loss64, loss_case, norm64, randn,
+                         within)
 
 
 def busy_stream():
@@ -153,3 +156,58 @@ def test_loss_gradients_of_tokens_with_very_different_weights(dt, aligned, T, pi
         small = (gv / gmax < 1e-5)[:, 0]
         e = (got - one).norm(dim=1)[small] / one.norm(dim=1)[small]
         assert float(e.median()) > 0.05
+
+
+# ---------------------------------------------------------------------------
+# gradients added straight into a reducer's main_grad
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("before", [5, 64])   # elements of the parameter before the table, as buckets pack them
+def test_table_gradients_go_straight_into_main_grad(before):
+    """Two replicas of a tied table: both gradients are added into fp32 views of main_grad, two micro-steps each, the
+    reducer averages what is there (the table has no gradient tensor of its own) and the clip scales it.
+
+    A gradient is off by what check_grads allows for each contribution; the average adds two roundings in fp32, the
+    clip the norm's and the factor's."""
+    W, V, dim, T = 2, 1009, 72, 300
+    other = [torch.full((before,), 0.25 + w, device=DEV) for w in range(W)]
+    r = BucketReducer([before, V * dim], None, W, D.DDP_ALLREDUCE, D.DDP_ORDER_REVERSE, 25 << 20, 1 << 20, 1,
+                      [[other[w], None] for w in range(W)], coalesce=True)
+    views = [r.view(1, w).view(V, dim) for w in range(W)]
+    e, f = lm.TokenEmbedding(V, dim, BF16, scale=3.0), lm.VocabLoss(V, dim, BF16)
+    table = randn(gen(90), V, dim, dtype=BF16, scale=0.3)
+    gl = torch.full((1,), 1.0 / T, device=DEV)
+    want, tol = torch.zeros(W, V, dim, dtype=torch.float64, device=DEV), torch.zeros(W, V, dim, dtype=torch.float64, device=DEV)
+    r.main_grad.zero_()
+    for w in range(W):
+        for micro in range(2):
+            ids = torch.randint(0, V, (T,), generator=gen(91 + 2 * w + micro), device=DEV)
+            y = (ids * 7 + 3) % V
+            h = e.forward(table, ids)
+            _, lse = f.forward(h, table, y)
+            dh, _ = f.backward(h, table, y, lse, gl, grad_weight=views[w], accumulate=True)
+            e.backward(dh, ids, grad_weight=views[w], accumulate=True)
+            q = loss64(h, table, y, torch.ones(T, dtype=torch.bool, device=DEV), gl.expand(T))
+            eg = q["dg"] + (U[BF16] + 4 * 2.0 ** -24 + (max(T, V) + 2) * 2.0 ** -23) * q["g"].abs() + 2.0 ** -133
+            s, mag = embed_grad64(dh, ids, V, 3.0, -1)
+            want[w] += q["g"].t() @ q["H"] + s
+            n = torch.bincount(ids, minlength=V).double()[:, None]
+            # (four additions to what is there, each rounded)
+            tol[w] += eg.t() @ q["H"].abs() + (n + 2) * 2.0 ** -24 * mag + 2.0 ** -22 * (q["g"].abs().t() @ q["H"].abs() + mag)
+    local = [v.clone() for v in views]
+    for w in range(W):
+        within(local[w], want[w], tol[w], f"replica {w}")
+    r.step(accumulate=True)
+    mean = local[0] * 0.5 + local[1] * 0.5
+    for w in range(W):
+        assert torch.equal(views[w], mean)
+        assert torch.equal(r.view(0, w), other[0] * 0.5 + other[1] * 0.5)
+    ref = norm64([r.view(0, 0), mean], False)
+    kept = mean.clone()
+    norms = [lm.GradClipper.of_reducer(r, w).clip(0.5 * ref) for w in range(W)]
+    for w in range(W):
+        assert abs(float(norms[w]) - ref) <= NORM_REL * ref
+        scaled = kept.double() * (0.5 * ref / (ref + 1e-6))
+        within(views[w], scaled, scaled.abs() * (NORM_REL + 5 * 2.0 ** -24) + TINY[F32], "clipped")
+    assert torch.equal(views[0], views[1])
+    assert D.ddp_lm_status() == 0
+    r.close()
