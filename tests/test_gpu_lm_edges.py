@@ -15,8 +15,15 @@ if not torch.cuda.is_available():  # pragma: no cover
 import allreduce_ddp_assign_gb300 as D
 from allreduce_ddp_assign_gb300 import lm
 from allreduce_ddp_assign_gb300.session import BucketReducer
-from test_gpu_lm import (BF16, DEV, F16, F32, NORM_REL, TINY, U, embed_grad64, gen, loss64, loss_case, norm64, randn,
-                         within)
+from test_gpu_lm import (BF16, DEV, F16, F32, NORM_REL, TINY, U, check_grads, embed_grad64, gen, loss64, loss_case, norm64,
+                         randn, within)
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    D.ddp_lm_status(reset=True)
+    yield
+    torch.cuda.synchronize()
 
 
 def busy_stream():
@@ -211,3 +218,84 @@ def test_table_gradients_go_straight_into_main_grad(before):
     assert torch.equal(views[0], views[1])
     assert D.ddp_lm_status() == 0
     r.close()
+
+
+# ---------------------------------------------------------------------------
+# paths that only certain sizes take
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,V,dim", [
+    (8300, 17003, 72),    # more than 32 row tiles, and two pieces of the vocabulary of the library's own choice
+    (200, 700, 8456),     # more than 32 tiles along the width
+])
+def test_loss_of_many_tiles(T, V, dim, dt):
+    h, w, y, valid = loss_case(100, T, V, dim, 0.05, dt)
+    f = lm.VocabLoss(V, dim, dt)
+    loss, lse = f.forward(h, w, y)
+    r = loss64(h, w, y, valid)
+    within(lse[valid], r["lse"], r["dlse"], "lse")
+    within(loss[valid], r["loss"], r["dloss"], "loss")
+    del r
+    gl = torch.rand(T, generator=gen(101), device=DEV)
+    gh, gw = f.backward(h, w, y, lse, gl)
+    check_grads(h, w, y, valid, gl, gh, gw, torch.zeros_like(gw), dt)
+    assert D.ddp_lm_status() == 0
+
+
+@pytest.mark.parametrize("T,V,dim", [
+    (5003, 300007, 12),    # more than 128 sorting CTAs
+    (100003, 200003, 6),   # the same, and more tokens than their places have room for in shared memory
+    (120001, 30522, 8),    # more tokens than room, 128 CTAs
+])
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64])
+@pytest.mark.parametrize("skip", [0, 1])   # ids that start off the 16-byte (8-byte) boundary
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_gradient_of_long_lists_and_large_tables(T, V, dim, idt, skip, accumulate):
+    g = gen(110)
+    ids = torch.randint(0, V, (T + skip,), generator=g, device=DEV)
+    ids = torch.where(torch.rand(T + skip, generator=g, device=DEV) < 0.3, ids % 50, ids)
+    ids[T // 3:T // 3 + 400] = 7   # the padding id
+    ids[11], ids[T // 2] = -3, V   # left out, and reported
+    ids = ids.to(idt)[skip:]
+    go = randn(g, T, dim)
+    base = randn(g, V, dim) if accumulate else torch.zeros(V, dim, device=DEV)
+    e = lm.TokenEmbedding(V, dim, F32, scale=1.5, padding_idx=7)
+    gw = e.backward(go, ids, grad_weight=base.clone(), accumulate=accumulate)
+    s, mag = embed_grad64(go, ids, V, 1.5, 7)
+    n = torch.bincount(ids[(ids >= 0) & (ids < V)].long(), minlength=V).double()[:, None]
+    tol = (n + 2) * 2.0 ** -24 * (mag + base.double().abs()) + TINY[F32]
+    within(gw, s + base.double(), torch.where(mag > 0, tol, torch.zeros_like(tol)))
+    assert torch.equal(gw, e.backward(go, ids.clone(), grad_weight=base.clone(), accumulate=accumulate))
+    assert D.ddp_lm_status(reset=True) == 2
+
+
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64])
+def test_targets_off_a_boundary(idt):
+    T, V, dim = 300, 900, 64
+    h, w, y, valid = loss_case(120, T, V, dim, 0.2, BF16)
+    f = lm.VocabLoss(V, dim, BF16)
+    off = torch.cat([y[:1], y]).to(idt)[1:]
+    loss, lse = f.forward(h, w, y)
+    gl = torch.rand(T + 1, generator=gen(121), device=DEV)[1:]
+    a, b = f.backward(h, w, y, lse, gl), f.backward(h, w, off, lse, gl)
+    assert all(torch.equal(p, q) for p, q in zip(f.forward(h, w, off) + b, (loss, lse) + a))
+
+
+@pytest.mark.parametrize("T,V,dim,ignored,dt", [
+    (864, 20000, 1086, 0.0, BF16), (2000, 9000, 512, 0.7, F16), (300, 30000, 128, 0.0, BF16), (8192, 3000, 64, 0.0, F16),
+])
+def test_each_of_many_calls_gives_the_same_bits(T, V, dim, ignored, dt):
+    """Calls without a pause between them, every one compared with the first; no wait runs out."""
+    h, w, y, _ = loss_case(130, T, V, dim, ignored, dt)
+    f = lm.VocabLoss(V, dim, dt)
+    loss, lse = f.forward(h, w, y)
+    gl = torch.full((1,), 1.0 / T, device=DEV)
+    gh, gw = f.backward(h, w, y, lse, gl)
+    assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(gw).all())
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(300):
+        l2, e2 = f.forward(h, w, y)
+        gh2, gw2 = f.backward(h, w, y, e2, gl)
+        differ += (l2 != loss).any() | (e2 != lse).any() | (gh2 != gh).any() | (gw2 != gw).any()
+    assert int(differ) == 0
+    assert D.ddp_lm_status() == 0
