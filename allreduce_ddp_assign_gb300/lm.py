@@ -47,9 +47,10 @@ def _dtype(t) -> int:
 
 def _here(x, name) -> None:
     """x lies on the current device, where the library launches."""
-    if not x.is_cuda:
+    at = x.get_device()   # -1: not on a GPU
+    if at < 0:
         raise ValueError(f"{name} is not on the GPU")
-    if x.get_device() != _current_device():
+    if at != _current_device():
         raise ValueError(f"{name} is on {x.device}, the current device is cuda:{_current_device()}")
 
 
@@ -70,7 +71,7 @@ def _rows(x, name, rows, dim, dtypes) -> int:
 def _ids(x, name) -> int:
     """Bytes of an id."""
     size = {torch.int64: 8, torch.int32: 4}.get(x.dtype)
-    if size is None or not x.is_cuda:
+    if size is None:
         raise ValueError(f"{name} must be int32 or int64 on the GPU")
     _here(x, name)
     if x.dim() != 1 or not x.is_contiguous():
@@ -87,7 +88,7 @@ def _lend(stream, *tensors) -> None:
 
 
 def _floats(x, name) -> None:
-    if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
+    if x.dtype != torch.float32 or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor on the GPU")
     _here(x, name)
 
