@@ -15,8 +15,14 @@
 //
 // Bound by the tensor cores: 2 T V D operations forward, 8 T V D for a step (6 without the
 // second z).  Measured on a GB300 (2 T V D = 632 GFLOP at 8192 tokens x 50257 words x 768,
-// bf16): a step 1.72 ms, 1.47 PFLOP/s.  At 4096 x 131072 x 4096 the step, seconds long, runs
-// at what the power limit leaves (1.63 PFLOP/s; cuBLAS for seconds: 1.74).
+// bf16): a step 1.73 to 1.85 ms, 1.46 to 1.37 PFLOP/s, the longer one back to back under the
+// power limit.  At 4096 x 131072 x 4096 the step, seconds long, runs at what that limit
+// leaves (10.6 ms, 1.63 PFLOP/s; cuBLAS for seconds: 1.74).
+//
+// Rounded to 16 bits on the way: G, the one rounding that a form in fp32 does not have.  The
+// tensor cores take 16-bit operands; G in two parts would double both gradient products.
+// It leaves the gradients about 1.2 times as far from the exact ones as one rounding of
+// the result alone (1.96e-3 beside 1.66e-3 in bf16, 2.55e-4 beside 2.07e-4 in fp16).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -35,7 +41,8 @@ constexpr int64_t kMaxVocab = (int64_t{1} << 31) - 512;
 constexpr int kFewTokens = 2;      // up to so many the forward pass goes without matrix products
 constexpr int kMaxFewCtas = 1024;
 // Elements of G that are held at a time: 537 MB.  More pieces are more launches, which cost
-// about 8 us each at their ends (the masked step at 30522 x 1024: 367 us with half of it, 340).
+// about 8 us each at their ends (with cold caches the masked step at 30522 x 1024 takes 400 us
+// with half of it, 352 so; 8192 tokens x 50257 x 768 1.765 ms and 1.75).
 constexpr int64_t kPieceElements = int64_t{1} << 28;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -359,9 +366,11 @@ copy_weight_kernel(const uint16_t* w, int64_t ws, int64_t vocab, int64_t dim, ui
 // Why so: a CTA's 128 x 256 share of a tile needs 32 KB of operands for 512 cycles of
 // products; alone, without the pair, it would need 48 KB, more than an SM gets from L2 in
 // that time.  Six stages are 192 KB; four to six made no difference.  What did: the code
-// written out for each use (466 -> 443 us forward at 8192 x 50257 x 768) and reading
-// ahead what dH and dW add to (masked step 480 -> 402).  Where k is short the epilogue is
-// the bound: 2.1 us a tile at 128 values of k, twice what its exponentials take.
+// written out for each use (466 -> 443 us forward at 8192 x 50257 x 768, when it came; 356
+// now) and reading ahead what dH and dW add to (masked step 480 -> 402 then, 298 now).
+// Where k is short the epilogue is the bound: 2.1 us a tile at 128 values of k, twice what
+// its exponentials take.  146 registers, one CTA an SM.  At 4096 x 16384 x 768 the tensor
+// pipe is active 68% of the time in the statistics, 59% in G, 83% in dH and dW.
 // what becomes of C, in the order in which a launch runs them
 enum Use { USE_DH, USE_DW, USE_GRAD, USE_STATS, kUses };
 
@@ -974,8 +983,8 @@ template <int DT> cudaError_t launch_products(const Batch& batch, cudaStream_t s
     }
     cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
     // (the cluster's size is the kernel's own.)  Neither this kernel nor the one after it is
-    // launched to start while the kernel before it ends: that gained nothing here (470 and 471
-    // us), and no CTA then takes over shared memory whose last owner's pair still runs.
+    // launched to start while the kernel before it ends: no CTA takes over shared memory
+    // whose last owner's pair still runs.
     cfg.numAttrs = 0;
     return cudaLaunchKernelEx(&cfg, product_kernel<DT>, batch);
 }
@@ -1052,8 +1061,9 @@ combine_kernel(const int32_t* count, const int32_t* rows, const float2* part, in
 // HBM-bound: the weight is read once, a warp takes four of its rows at a time and
 // multiplies them with every token's hidden state, which shared memory holds.  One CTA an
 // SM, with 128 KB of the weight on its way all the time.  At 50257 x
-// 768 with cold caches one token takes 27 us (50 on the tensor cores; the read alone 17.5
-// us, 4.4 TB/s) and two 30; four took 66 (52) with registers instead of the ring.
+// 768 one token takes 27 us with cold caches (50 on the tensor cores; this kernel alone 17.5
+// us, 4.4 TB/s), 22 back to back, and two 30 (cold); four took 66 (52) with registers
+// instead of the ring.
 constexpr int kFewElements = 32768;  // of hidden states in shared memory
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;

@@ -199,7 +199,10 @@ class GradClipper:
 
 
 class TokenEmbedding:
-    """Lookup in a [vocab, dim] table with a scale, and the table's gradient."""
+    """Lookup in a [vocab, dim] table with a scale, and the table's gradient.
+
+    padding_idx  the id whose row gets no gradient (None or negative: none).
+    """
 
     def __init__(self, vocab, dim, dtype, scale=1.0, padding_idx=None):
         self.vocab, self.dim, self.torch_dtype, self.dtype = int(vocab), int(dim), dtype, _dtype(dtype)

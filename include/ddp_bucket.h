@@ -875,8 +875,12 @@ void ddp_plan_destroy(ddp_plan* plan);
  * Common to these calls: matrices are row-major with a row stride in elements
  * (>= the row length); token ids and targets are DEVICE int32 (id_bytes = 4) or
  * int64 (id_bytes = 8); sums, norms and softmax statistics are fp32 or wider and
- * every result is rounded once to its type; every sum is taken in an order that
- * depends on the sizes alone, so equal calls give equal bits.  An id outside
+ * every result is rounded once to its type; every sum is taken in a fixed order, so
+ * equal calls give equal bits.  That order follows from the sizes, from where the
+ * tensors lie within 16 bytes, from the GPU's number of SMs and, in grad_hidden, from how
+ * many tokens have a target: the same values at another alignment or on another GPU
+ * may give another last bit (replicas that must clip by the very same factor
+ * need their buffers aligned alike, as main_grad copies are).  An id outside
  * [0, vocab) cannot be refused on the host: the kernels read and write nothing
  * through it, treat its token as described at each call, and set bit 1 of the
  * word that ddp_lm_status reads.  `workspace` is DEVICE scratch of at least
@@ -920,7 +924,8 @@ ddp_status ddp_grad_norm(const void* const* grads, const int64_t* offset, const 
  *         that tensor is not written); out == NULL: in place.  An output is its
  *         own input or does not overlap any input.  In place, nothing is
  *         written when the factor is 1.  A norm of infinity gives the factor 0
- *         (infinite elements become NaN), a NaN norm makes every element NaN.
+ *         (infinite elements become NaN), a NaN norm, or an infinite one with
+ *         max_norm infinite too, makes every element NaN.
  *   norm  DEVICE float[1]: the norm before clipping.
  * Errors: as ddp_grad_norm; DDP_E_INVAL for a max_norm that is negative or NaN.
  */
@@ -985,7 +990,10 @@ ddp_status ddp_vocab_loss_workspace(int64_t ntokens, int64_t vocab, int64_t dim,
  *   hidden   DEVICE dtype [ntokens x dim], rows hidden_stride apart.
  *   weight   DEVICE dtype [vocab x dim], rows weight_stride apart.
  *   loss, lse  DEVICE float[ntokens].
- * dtype is DDP_BF16 or DDP_F16; products are exact and summed in fp32.
+ * dtype is DDP_BF16 or DDP_F16; products are exact and summed in fp32, for three tokens
+ * and more on the tensor cores, which cut off low bits at each step of dim (lse is off
+ * by about 3e-7 of itself at dim 768, 6e-6 at 4096); the target's logit is then summed
+ * again with fp32 multiply-adds, for loss and lse.  Logits stay below 2^127.
  * ntokens < 2^31 - 4096, vocab < 2^31 - 512, dim < 2^24.
  * Errors: DDP_E_INVAL (negative sizes, vocab or dim < 1, a stride below dim,
  * another dtype, id_bytes, a NULL pointer with ntokens > 0, too small a
@@ -999,6 +1007,7 @@ ddp_status ddp_vocab_loss_forward(const void* hidden, int64_t hidden_stride, con
 /*
  * ddp_vocab_loss_backward -- gradients of sum_t grad_loss[t] * loss[t]:
  *   G[t][v] = grad_loss[t] * (exp(z[t][v] - lse[t]) - [v == targets[t]])
+ *             (0 where grad_loss[t] is 0, whatever z)
  *   grad_hidden = G x weight,   grad_weight (= | +=) G^T x hidden
  * with z computed again and G held for one piece of the vocabulary at a time,
  * rounded to `dtype` after division by the largest finite |grad_loss| (that factor is
