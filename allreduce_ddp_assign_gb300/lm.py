@@ -587,7 +587,7 @@ class AdamW:
             self.exp_avg_scale, self.exp_avg_sq_scale = (torch.zeros(n, device=self.device) for _ in range(2))
         self._moments = [None if t is None else t.data_ptr() for t in
                          (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)]
-        self._streams = {_raw_stream(self.device.index)}   # those on which the allocator knows the memory in use
+        self._streams = set()   # those on which the allocator knows all of this memory in use
 
     @classmethod
     def of_reducer(cls, reducer, params, w=0, **kw):
@@ -610,10 +610,7 @@ class AdamW:
             return
         if self.device.index != _current_device():
             raise ValueError(f"the parameters are on {self.device}, the current device is cuda:{_current_device()}")
-        on = _raw_stream(self.device.index)
-        if on not in self._streams:
-            self._lend_all(torch.cuda.current_stream(self.device))
-            self._streams.add(on)
+        on = self._stream()
         lr_at = norm_at = None
         if lr is None:
             lr = self.lr
@@ -635,9 +632,15 @@ class AdamW:
             raise ValueError(f"{name} has {t.numel()} elements")
         return t.data_ptr()
 
-    def _lend_all(self, stream):
-        _lend(stream, self._tables, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale,
-              *self._tensors[0], *self._tensors[1], *self._tensors[2])
+    def _stream(self):
+        """The current stream's handle.  Before its first use there the allocator learns that all of the memory is: the
+        moments and tables are of the stream that the object was made on, the caller's tensors of any."""
+        on = _raw_stream(self.device.index)
+        if on not in self._streams:
+            _lend(torch.cuda.current_stream(self.device), self._tables, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
+                  self.exp_avg_sq_scale, *self._tensors[0], *self._tensors[1], *self._tensors[2])
+            self._streams.add(on)
+        return on
 
     def steps(self) -> int:
         """The steps taken (waits for the current stream)."""
@@ -645,6 +648,7 @@ class AdamW:
 
     def moments(self, k):
         """(m, v) of parameter k in fp32, in its shape: copies."""
+        self._stream()
         p = self._tensors[0][k]
         rows = slice(int(self.first_block[k]), int(self.first_block[k + 1]))
         m, v = (x[rows].to(torch.float32, copy=True) for x in (self.exp_avg, self.exp_avg_sq))
@@ -654,6 +658,7 @@ class AdamW:
 
     def state_dict(self):
         """The steps taken and copies of the moments as they are held."""
+        self._stream()
         d = {"step": self.steps(), "exp_avg": self.exp_avg.clone(), "exp_avg_sq": self.exp_avg_sq.clone()}
         if self.state_bits == 8:
             d.update(exp_avg_scale=self.exp_avg_scale.clone(), exp_avg_sq_scale=self.exp_avg_sq_scale.clone())
@@ -670,6 +675,7 @@ class AdamW:
                 raise ValueError(f"{name} is {new.dtype} {tuple(new.shape)}, expected {mine.dtype} {tuple(mine.shape)}")
         if int(state["step"]) < 0:
             raise ValueError(f"{state['step']} steps")
+        self._stream()
         for name in names:
             getattr(self, name).copy_(state[name])
         self._tables[0] = int(state["step"])

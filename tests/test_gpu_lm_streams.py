@@ -1,0 +1,40 @@
+"""Objects made on a stream that their tensors do not come from: memory stays in use until the work there is done."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from allreduce_ddp_assign_gb300 import lm
+from test_gpu_adamw import Problem
+from test_gpu_lm import BF16, F32
+
+
+def dropped_while_queued(tensors, make, use):
+    """make() and use(object) on a side stream that is busy; the caller's `tensors` are then dropped with the object, and
+    others of their sizes made on their own stream."""
+    places = {t.data_ptr() for t in tensors}
+    sizes = [(t.shape, t.dtype, t.device) for t in tensors]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o = make()
+        torch.cuda._sleep(1_000_000_000)
+        use(o)
+    del o
+    tensors.clear()
+    new = [torch.empty(*z[:1], dtype=z[1], device=z[2]) for z in sizes for _ in range(3)]
+    waiting = not s.query()
+    assert not places & {t.data_ptr() for t in new}
+    assert waiting   # else the check says nothing
+    s.synchronize()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_optimizer_made_on_another_stream(bits):
+    q = [Problem(11, [3001, 70, 5000], F32, F32, BF16, 0)]
+    q[0].before.clear()
+    tensors = list(q[0].flat.values())
+    dropped_while_queued(tensors, lambda: q.pop().optimizer(state_bits=bits), lambda opt: opt.step())
