@@ -149,7 +149,7 @@ class GradClipper:
         at = self._tables.data_ptr() + 8 * np.cumsum([0] + [len(p) for p in parts])
         self.offset, self.grads_tab, out_tab, self.dtypes = (int(a) for a in at[:4])
         self.out_tab = None if out is None else out_tab
-        self._streams = {_raw_stream(self.device.index)}   # those on which the allocator knows the memory in use
+        self._streams = set()   # those on which the allocator knows all of this memory in use
 
     @classmethod
     def of_reducer(cls, reducer, w=0, norm_type=2.0):
@@ -163,8 +163,8 @@ class GradClipper:
 
     def _stream(self):
         """The current stream's handle.  The tables were allocated on the stream that was current when they
-        were made; on another one the allocator has to learn of their use, or it gives their memory away, while
-        the kernels still read it, when the object and its tensors are dropped."""
+        were made, the caller's tensors on any; on another one the allocator has to learn of their use, or it gives
+        their memory away, while the kernels still read it, when the object and its tensors are dropped."""
         if self.device.index != _current_device():
             raise ValueError(f"the gradients are on {self.device}, the current device is cuda:{_current_device()}")
         raw = _raw_stream(self.device.index)

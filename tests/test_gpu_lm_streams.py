@@ -38,3 +38,19 @@ def test_an_optimizer_made_on_another_stream(bits):
     q[0].before.clear()
     tensors = list(q[0].flat.values())
     dropped_while_queued(tensors, lambda: q.pop().optimizer(state_bits=bits), lambda opt: opt.step())
+
+
+@pytest.mark.parametrize("out", [False, True])
+def test_a_clipper_made_on_another_stream(out):
+    tensors = list(Problem(12, [3001, 70, 5000], F32, F32, BF16, 0).flat.values())
+    g, o = [tensors[0], tensors[1], tensors[2]], [torch.empty_like(t) for t in tensors] if out else None
+    tensors += o or []
+
+    def make():
+        c = lm.GradClipper(g, out=o)
+        g.clear()
+        if o:
+            o.clear()
+        return c
+
+    dropped_while_queued(tensors, make, lambda c: c.clip(1.0))

@@ -78,3 +78,18 @@ def test_a_state_loaded_or_copied_on_another_stream_lends_it_the_moments(lent, b
         lent.current = 20 + k
         use()
         assert lent.to(20 + k) >= {id(t) for t in (opt.exp_avg, opt.exp_avg_sq, opt._tables)}
+
+
+@pytest.mark.parametrize("call", [lambda c: c.norm(), lambda c: c.clip(1.0)])
+@pytest.mark.parametrize("out", [False, True])
+def test_a_call_on_the_stream_the_clipper_was_made_on_lends_it_everything(lent, monkeypatch, call, out):
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: empty(*a, **kw))
+    g = [Kept((5,), F32), None, Kept((300,), BF16)]
+    o = [Kept((5,), F32), None, None] if out else None
+    c = lm.GradClipper(g, out=o)
+    call(c)
+    assert lent.to(7) == {id(t) for t in (c._tables, g[0], g[2], *(o or ())) if t is not None}
+    told = len(lent)
+    call(c)
+    assert len(lent) == told   # once
