@@ -481,11 +481,12 @@ class LayerNorm:
                     raise ValueError(f"grad_bias has dtype {grad_bias.dtype}, grad_weight {kind}")
         size = 0
         if need_weight or need_bias:
-            size = self._sizes.get(n)
+            key = n, s.get_device()   # (it depends on the number of SMs)
+            size = self._sizes.get(key)
             if size is None:
                 if len(self._sizes) >= 64:
                     self._sizes.clear()
-                size = self._sizes[n] = ddp_layer_norm_workspace(n, dim)
+                size = self._sizes[key] = ddp_layer_norm_workspace(n, dim)
             memory = _empty(size, dtype=torch.uint8, device=s.device)
             scratch = memory.data_ptr()
         at = stats.data_ptr()
