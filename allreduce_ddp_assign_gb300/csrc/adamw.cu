@@ -753,14 +753,16 @@ extern "C" ddp_status ddp_adamw_step(const ddp_adamw_tensor* tensors, const int6
     if (!lr_at && !(lr >= 0. && lr <= 3e38)) return fail(DDP_E_INVAL, "%s: lr = %g", fn, lr);
     if (!(beta1 >= 0. && beta1 < 1.)) return fail(DDP_E_INVAL, "%s: beta1 = %g is not in [0, 1)", fn, beta1);
     if (!(beta2 >= 0. && beta2 < 1.)) return fail(DDP_E_INVAL, "%s: beta2 = %g is not in [0, 1)", fn, beta2);
-    if (!(eps >= 0. && eps <= 3e38)) return fail(DDP_E_INVAL, "%s: eps = %g", fn, eps);
-    if (!(grad_scale > 0. && grad_scale <= 3e38)) return fail(DDP_E_INVAL, "%s: grad_scale = %g", fn, grad_scale);
+    // (a divisor below 2^-126 would be taken for 0)
+    if (!(eps == 0. || (eps >= 0x1p-126 && eps <= 3e38))) return fail(DDP_E_INVAL, "%s: eps = %g", fn, eps);
+    // (neither it nor its reciprocal overflows)
+    if (!(grad_scale >= 1. / 3e38 && grad_scale <= 3e38)) return fail(DDP_E_INVAL, "%s: grad_scale = %g", fn, grad_scale);
     if (norm && !(max_norm >= 0.)) return fail(DDP_E_INVAL, "%s: max_norm = %g is negative or NaN", fn, max_norm);
     const StepArgs a{tensors, first_block, ntensors, nblocks, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, state,
                      lr_at, norm, static_cast<float>(lr), static_cast<float>(beta1), static_cast<float>(beta2),
                      static_cast<float>(1. - beta1), static_cast<float>(1. - beta2), static_cast<float>(std::log(beta1)),
                      static_cast<float>(std::log(beta2)), static_cast<float>(eps), static_cast<float>(1. / grad_scale),
-                     static_cast<float>(max_norm), seed, 1.f};
+                     max_norm > 3e38 ? INFINITY : static_cast<float>(max_norm), seed, 1.f};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch(a, state_bits == 8, s);
     if (e != cudaSuccess) return fail(DDP_E_CUDA, "%s: kernel launch failed: %s", fn, cudaGetErrorString(e));

@@ -1141,8 +1141,8 @@ typedef struct ddp_adamw_tensor {
  * Parameters, copies and gradients lie anywhere and do not overlap.  Up to 12 bytes beside a
  * block of 256 values may be read and not used, inside its tensor; nothing else is written.
  * Errors: DDP_E_INVAL (negative sizes, NULL tables or moments, unknown state_bits, beta1 or
- * beta2 outside [0, 1), a negative or NaN lr, eps or max_norm, a grad_scale that is not
- * positive); DDP_E_CUDA.
+ * beta2 outside [0, 1), a negative or NaN lr, eps or max_norm, an eps between 0 and 2^-126, a
+ * grad_scale that is not positive or whose reciprocal is above 3e38); DDP_E_CUDA.
  */
 ddp_status ddp_adamw_step(const ddp_adamw_tensor* tensors, const int64_t* first_block, int32_t ntensors,
                           int64_t nblocks, void* exp_avg, void* exp_avg_sq, float* exp_avg_scale,

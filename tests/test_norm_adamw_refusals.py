@@ -91,6 +91,15 @@ def test_adamw(match, change):
     refused(match, D.ddp_adamw_step, STEP, **change)
 
 
+@pytest.mark.parametrize("match,change", [
+    # its reciprocal, which the gradients are multiplied by, would be infinite
+    ("grad_scale", dict(grad_scale=1e-39)), ("grad_scale", dict(grad_scale=5e-324)),
+    # the step's quotient takes a divisor below 2^-126 for 0, and 0 / 0 is not 0
+    ("eps", dict(eps=1e-60)), ("eps", dict(eps=2.0 ** -127))])
+def test_adamw_numbers_that_fp32_does_not_hold(match, change):
+    refused(match, D.ddp_adamw_step, STEP, **change)
+
+
 def test_objects_refuse_on_the_host():
     torch = pytest.importorskip("torch")
     from allreduce_ddp_assign_gb300 import lm
