@@ -25,15 +25,19 @@ def dropped_while_queued(tensors, make, use):
         use(o)
     del o
     tensors.clear()
-    new = [torch.empty(*z[:1], dtype=z[1], device=z[2]) for z in sizes for _ in range(3)]
+    new = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype, device in sizes for _ in range(3)]
     waiting = not s.query()
-    assert not places & {t.data_ptr() for t in new}
     assert waiting   # else the check says nothing
+    assert not places & {t.data_ptr() for t in new}
     s.synchronize()
 
 
 @pytest.mark.parametrize("bits", [32, 8])
 def test_an_optimizer_made_on_another_stream(bits):
+    warm = Problem(11, [3001, 70, 5000], F32, F32, BF16, 0)
+    warm.optimizer(state_bits=bits).step()   # (a kernel's first launch waits for the whole GPU)
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
     q = [Problem(11, [3001, 70, 5000], F32, F32, BF16, 0)]
     q[0].before.clear()
     tensors = list(q[0].flat.values())
@@ -42,6 +46,10 @@ def test_an_optimizer_made_on_another_stream(bits):
 
 @pytest.mark.parametrize("out", [False, True])
 def test_a_clipper_made_on_another_stream(out):
+    warm = [torch.ones(100, device="cuda") for _ in range(2)]
+    lm.GradClipper(warm[:1], out=warm[1:] if out else None).clip(1.0)
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
     tensors = list(Problem(12, [3001, 70, 5000], F32, F32, BF16, 0).flat.values())
     g, o = [tensors[0], tensors[1], tensors[2]], [torch.empty_like(t) for t in tensors] if out else None
     tensors += o or []
