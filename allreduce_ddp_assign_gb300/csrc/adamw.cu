@@ -76,9 +76,10 @@ __device__ __forceinline__ Common common_of(const StepArgs& a)
     c.g = a.inv_scale;
     c.skip = false;
     if (a.norm) {
-        const float norm = *a.norm * a.inv_scale;
+        // (operations of their own: codes in 8 bits depend on each rounding)
+        const float norm = __fmul_rn(*a.norm, a.inv_scale);
         c.skip = !(fabsf(norm) < INFINITY);
-        const float ratio = a.max_norm / (norm + 1e-6f);
+        const float ratio = __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f));
         c.g *= ratio > 1.f ? 1.f : ratio;
     }
     // 1 - b^t without the cancellation at small t
@@ -372,8 +373,8 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c)
     return r;
 }
 
-// The square roots of v = (v0, v1), from the hardware's reciprocal one and its remainder (Markstein, 1990): rounded once, but
-// for an ulp in some of the smallest.
+// The square roots of v = (v0, v1), from the hardware's reciprocal one and its remainder (Markstein, 1990): rounded once from
+// 2^-102 on, where the remainder is exact (compared for every normal number), off by an ulp or two in some below.
 __device__ __forceinline__ Two roots_of(Two v, float v0, float v1)
 {
     float y0, y1;
@@ -424,7 +425,7 @@ __device__ __forceinline__ float scale_of(const float (&f)[kEach])
     float top = larger(larger(larger(f[0], f[1]), larger(f[2], f[3])), larger(larger(f[4], f[5]), larger(f[6], f[7])));
     // (as whole numbers magnitudes are in the same order, NaN last)
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    const float s = top * (1.f / kE4m3Max);
+    const float s = top * (1.f / kE4m3Max);   // (a product by the rounded reciprocal is the format's own rule)
     return s < 0x1p-126f ? 0.f : s;   // (its reciprocal is finite; a block below that is held as zeros)
 }
 
@@ -443,8 +444,8 @@ __device__ __forceinline__ void chances_of(uint32_t* to, uint64_t z)
 // fraction of a step to which the chance is added; all of it is moved up by 4 to put the code into a byte.
 // The largest, 14 steps of its binade, is off by 2 2^-24 of itself at most, and the largest chance is 2^-17 short of a step,
 // so that no finite value gets past 448.
-// All that decides a code is rounded as its formula is written, one operation after the other, so that the codes are those of
-// any other program that does the same: an ulp would be a step of 6 to 12% for a few values in a million.
+// All that decides a code is rounded to fp32 operation by operation, in the order that the declaration gives, so that the codes
+// are those of any other program that does the same: an ulp would be a step of 6 to 12% for a few values in a million.
 // FLOOR: what is not zero is held as the smallest code at least.
 template <bool FLOOR> __device__ __forceinline__ uint2 to_codes(const float (&f)[kEach], float scale, const uint32_t (&chance)[kEach])
 {
@@ -452,7 +453,8 @@ template <bool FLOOR> __device__ __forceinline__ uint2 to_codes(const float (&f)
     float x[kEach];
 #pragma unroll
     for (int j = 0; j < kEach; j += 2) {
-        // the quotient, rounded once: a product with the reciprocal and its remainder (Markstein, 1990)
+        // the quotient, rounded once: a product with the reciprocal and its remainder (Markstein, 1990), which is exact for
+        // values from 2^-101 on
         const Two y(f[j], f[j + 1]), q = y * Two(inv);
         (fma2(fma2(q, Two(-scale), y), Two(inv), q) * Two(0x1p-120f)).get(x[j], x[j + 1]);
     }

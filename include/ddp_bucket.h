@@ -1117,15 +1117,23 @@ typedef struct ddp_adamw_tensor {
  * state_bits 32: the moments are float[nblocks * DDP_ADAMW_BLOCK].  state_bits 8: they are
  * e4m3 values (1, 4 and 3 bits) of which value i stands for itself times the scale of its
  * block i / DDP_ADAMW_BLOCK; exp_avg holds m, exp_avg_sq the square root of v.  A block's
- * scale is its largest magnitude / 448.  Values are rounded up or down by chance so that their
- * means are kept (a moment follows changes far below a step of 8 bits); the chances follow
- * from seed, t and the value's place alone: with mix the finaliser of splitmix64 and G its
- * increment, value i of a moment adds, before it is cut off, (k + 1/2) / 2^16 of a step,
- * k = bits 16 (i mod 4) and on of mix(mix(seed + (t + 1) G) + (i / 4 + 1) G), where i is i xor 1
- * for exp_avg.  The step uses the moments before they are rounded.  A root that is not zero is
- * held as the smallest code at least; an m below 2^-117 in the whole block is held as 0.  A
- * gradient that is not finite, without a norm that tells, makes its block's moments NaN or
- * infinite.  A gradient times c above 2^63 makes v infinite.
+ * scale is its largest magnitude times fp32's 1/448, 0 where that is below 2^-126.  Values are
+ * rounded up or down by chance so that their means are kept (a moment follows changes far
+ * below a step of 8 bits); the chances follow from seed, t and the value's place alone: with
+ * mix the finaliser of splitmix64 and G its increment, value i of a moment adds, before it is
+ * cut off, (k + 1/2) / 2^16 of a step, k = bits 16 (i mod 4) and on of
+ * mix(mix(seed + (t + 1) G) + (i / 4 + 1) G), where i is i xor 1 for exp_avg.  The step uses the
+ * moments before they are rounded.  A root that is not zero is held as the smallest code at
+ * least; an m below 2^-117 in the whole block is held as 0.  A gradient that is not finite,
+ * without a norm that tells, makes its block's moments NaN or infinite.  A gradient times c of
+ * 2^64 or more makes v infinite.
+ *
+ * Scales and codes are those of any program that rounds to fp32 after each operation of: 1 - beta
+ * and 1 / grad_scale (from double), the norm times that, c, that times c, grad times the product,
+ * code * scale, beta1 m + (1 - beta1) g, beta2 (r r) + (1 - beta2)(g g) with r the
+ * root held, its root, the scale above, the quotient by it, and, below 2^-6 (where a step is 2^-9),
+ * that quotient to a multiple of 2^-29.  (Where a block has a v between 0 and 2^-102, or its largest
+ * m is below 2^-62, an ulp of a root or quotient may differ.)
  *
  *   tensors      DEVICE table of ntensors records.
  *   first_block  DEVICE int64[ntensors + 1], first_block[0] = 0, first_block[ntensors] =
