@@ -324,3 +324,36 @@ def test_many_rows(T, D, stride, off, dt, wdt, both):
     if both:
         again = f.forward(x, w, b, residual=r, sum_out=x, out=r)
         assert all(torch.equal(p, q) for p, q in zip(again, (y, s, stats)))
+
+
+@pytest.mark.parametrize("T,D,stride,off", [(1300, 8201, 8201, 0), (700, 16391, 16392, 3), (700, 16392, 16392, 0), (1300, 12288, 12288, 0),
+                                            (300, 65537, 65537, 1)])
+@pytest.mark.parametrize("dt,wdt", [(F32, F32), (BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("both", [False, True])
+def test_many_rows_that_no_team_holds(T, D, stride, off, dt, wdt, both):
+    """Several rows a CTA where a whole CTA goes over a row in passes (more rows than 4 an SM; 65537 columns, whose sums
+    take a row of the workspace each, have 127 CTAs in the backward pass); 12288 columns of fp32 with a residual among
+    them, and fp32 rows that stay in registers."""
+    g = gen(21)
+    x, r, dy = (guarded(T, D, stride, dt, off)[1] for _ in range(3))
+    for t in (x, r, dy):
+        t.copy_(randn(g, T, D))
+    w, b = randn(g, D, dtype=wdt), randn(g, D, dtype=wdt)
+    f = lm.LayerNorm(D, dt, eps=EPS)
+    y, s, stats = f.forward(x, w, b, residual=r if both else None)
+    assert torch.equal(s, (x.float() + r.float()).to(dt) if both else x)
+    check_forward(s, w, b, EPS, y, stats, dt)
+    gx, gw, gb = f.backward(dy, s, w, stats, grad_sum=r if both else None)
+    check_backward(s, dy, w, stats, r if both else None, gx, gw, gb, None, dt)
+    # onto what is there, and over an input
+    base = [randn(g, D) for _ in range(2)]
+    gw, gb = (t.clone() for t in base)
+    buf, over = guarded(T, D, stride, dt, off)
+    over.copy_(dy)
+    f.backward(over, s, w, stats, grad_sum=r if both else None, grad_x=over, grad_weight=gw, grad_bias=gb, accumulate=True)
+    assert torch.equal(over, gx)
+    check_backward(s, dy, w, stats, r if both else None, over, gw, gb, base, dt)
+    assert_guard(buf, over)
+    if both:
+        again = f.forward(x, w, b, residual=r, sum_out=x, out=r)
+        assert all(torch.equal(p, q) for p, q in zip(again, (y, s, stats)))
