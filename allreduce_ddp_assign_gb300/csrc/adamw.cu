@@ -111,7 +111,7 @@ __device__ __forceinline__ float quotient(float x, float y)
 // from where the block lies:
 //   WHOLE    256 values on a 16-byte boundary: vectors;
 //   SHIFTED  256 values off a boundary (tensors packed tight), others of the tensor before and behind them: the vectors
-//            that cover them, whose words the lanes pass on to their neighbours.  The covering vectors hold up to 12
+//            that cover them, whose words the lanes pass on to their neighbours.  The covering vectors hold up to 14
 //            bytes of the values beside the block as well, which other warps may be stepping; they are not used;
 //   STRIDED  a tensor's first block off a boundary, its last block: single values, lane + 32 j, exchanged through 1 KB of
 //            shared memory of the warp.
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) adamw_kernel(const __grid_co
                 const float x = g[j] * c.g;
                 m[j] = fmaf(a.b1, m[j], a.one_b1 * x);
                 v[j] = fmaf(a.b2, v[j], a.one_b2 * (x * x));
-                                // (one rounding at the parameter's size)
+                // (one rounding at the parameter's size)
                 p[j] -= fmaf(decay, p[j], quotient(c.step * m[j], fmaf(root_of(v[j]), c.root, a.eps)));
             }
             store(pp, pd, pm, n, p, room, lane);

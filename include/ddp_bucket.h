@@ -1051,7 +1051,10 @@ ddp_status ddp_vocab_loss_backward(const void* hidden, int64_t hidden_stride, co
  *   weight, bias DEVICE w_dtype [dim]; bias NULL: none.  w_dtype is dtype or DDP_F32.
  *   mean, rstd   DEVICE float[ntokens].
  * Sums are fp32, the deviations taken around the mean.  A row with a NaN or an infinity
- * becomes NaN, and only it.  A row of equal values has rstd = 1 / sqrt(eps).
+ * becomes NaN, and only it.  A row of equal values has rstd = 1 / sqrt(eps).  Rows that are
+ * strided or off 16-byte boundaries are read in 16-byte pieces: up to 15 bytes beside a row,
+ * between the first row's begin and the last one's end, may be read and not used.  (The same
+ * holds for the backward pass.)
  * ntokens < 2^31 - 4096, dim <= 2^24.
  * Errors: DDP_E_INVAL (negative sizes, dim < 1, a stride below dim, an unknown dtype
  * or w_dtype, an eps that is negative, infinite or NaN, a residual without a sum or a sum
@@ -1146,7 +1149,7 @@ typedef struct ddp_adamw_tensor {
  *   lr_at        DEVICE float: the learning rate; NULL: lr.
  *   seed         of the chances (state_bits 8).
  *   norm         DEVICE float: the norm of the gradients as they are; NULL: no clipping.
- * Parameters, copies and gradients lie anywhere and do not overlap.  Up to 12 bytes beside a
+ * Parameters, copies and gradients lie anywhere and do not overlap.  Up to 14 bytes beside a
  * block of 256 values may be read and not used, inside its tensor; nothing else is written.
  * Errors: DDP_E_INVAL (negative sizes, NULL tables or moments, unknown state_bits, beta1 or
  * beta2 outside [0, 1), a negative or NaN lr, eps or max_norm, an eps between 0 and 2^-126, a
