@@ -363,6 +363,8 @@ class LayerNorm:
 
     def __init__(self, dim, dtype, eps=1e-5):
         self.dim, self.torch_dtype, self.dtype, self.eps = int(dim), dtype, _dtype(dtype), float(eps)
+        if self.dim < 1:
+            raise ValueError(f"dim = {dim}")
         self._same = (dtype,)
         self._wide = (dtype, torch.float32)
         self._sizes = {}

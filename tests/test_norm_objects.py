@@ -21,3 +21,9 @@ def test_the_workspace_is_that_of_the_gpu_at_hand(two_gpus, monkeypatch):   # no
         m, c, stats = (lambda: OnGpu((T, DIM), BF16, device)), (lambda: OnGpu((DIM,), F32, device)), OnGpu((2, T), F32, device)
         f.backward(m(), m(), c(), stats, grad_x=m(), grad_weight=c(), grad_bias=c())
     assert asked == [1000, 2000, 1000, 2000]
+
+
+def test_a_width_below_one_is_refused():
+    for dim in (0, -8):
+        with pytest.raises(ValueError, match="dim"):
+            lm.LayerNorm(dim, BF16)
