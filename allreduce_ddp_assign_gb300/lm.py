@@ -18,6 +18,7 @@ way there: attributes are read once, and addresses go to the library as integers
 from __future__ import annotations
 
 import math
+import numbers
 
 import numpy as np
 import torch
@@ -549,10 +550,10 @@ class AdamW:
             raise ValueError(f"state_bits {state_bits} is neither 8 nor 32")
         if len(grads) != len(params) or len(copies) != len(params):
             raise ValueError(f"{len(grads)} gradients and {len(copies)} copies for {len(params)} parameters")
-        decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
+        decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, numbers.Real) else [float(d) for d in weight_decay]
         if len(decays) != len(params):
             raise ValueError(f"{len(decays)} weight decays for {len(params)} parameters")
-        if not all(0.0 <= d < math.inf for d in decays):
+        if not all(0.0 <= d <= 3e38 for d in decays):   # (fp32)
             raise ValueError("a weight decay is negative or not finite")
         table = np.zeros(len(params), _RECORD)
         for k, (p, g, c) in enumerate(zip(params, grads, copies)):
