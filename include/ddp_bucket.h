@@ -1052,7 +1052,7 @@ ddp_status ddp_vocab_loss_backward(const void* hidden, int64_t hidden_stride, co
  *   mean, rstd   DEVICE float[ntokens].
  * Sums are fp32, the deviations taken around the mean.  A row with a NaN or an infinity
  * becomes NaN, and only it.  A row of equal values has rstd = 1 / sqrt(eps).  Rows that are
- * strided or off 16-byte boundaries are read in 16-byte pieces: up to 15 bytes beside a row,
+ * strided or off 16-byte boundaries are read in 16-byte pieces: up to 14 bytes beside a row,
  * between the first row's begin and the last one's end, may be read and not used.  (The same
  * holds for the backward pass.)
  * ntokens < 2^31 - 4096, dim <= 2^24.
