@@ -19,13 +19,13 @@
 //
 // Measured on a GB300 (graph replays).  32 bits, HBM-bound: 334M fp32 parameters with bf16 copies
 // 1.56 ms (10.0 GB, 6.4 TB/s, 0.94 of the copy; three CTAs an SM 1.64, a ring as in 8 bits 1.69);
-// 124M bf16 parameters and gradients 425 us (6.4 TB/s); 298M fp32 off boundaries 1.22 ms (6.2 TB/s);
-// 0.3M in 17 tensors 6.2 us.  8 bits, bound by instructions (590 a lane and block of 256 before the
+// 124M bf16 parameters and gradients 427 us (6.4 TB/s); 292M fp32 off boundaries 1.26 ms (6.5 TB/s, as
+// on them), with bf16 copies 1.39; 0.3M in 17 tensors 6.2 us.  8 bits, bound by instructions (590 a lane and block of 256 before the
 // roots and quotients were rounded exactly: 123 for the codes, 91 for conversions, 76 for the step,
 // 66 for chances and scales, the rest the ring's): 124M fp32 parameters with bf16 copies 420 us
-// (5.3 TB/s; three slots 508), bf16 ones without copies 394 us (3.2 TB/s; 332 with the hardware's
-// roots and a product for each quotient, whose codes differ for a few values in a million), 9M bf16
-// off boundaries 58 us (51).
+// (5.3 TB/s; three slots 508), bf16 ones without copies 396 us (3.1 TB/s; 312 with the hardware's
+// roots and a product for each quotient, whose codes differ for a few values in a million), 14M bf16
+// off boundaries 58 us (49).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(TW > kWarps ? 32 * TW : 32 * kWarps, TW > kWar
 }
 
 // Rows that no team holds: three passes over the row, which L2 keeps, in batches of columns whose loads are on their way
-// together.
+// together.  Bound by the instructions and latencies of single elements: 1.1 TB/s in 16 bits (8192 x 12001 with residual
+// 704 us), 5.0 in fp32 (4096 x 12288 with residual 160).
 constexpr int kBatch = 8;
 template <int DT> __global__ void __launch_bounds__(kLoopThreads) norm_loop_kernel(const __grid_constant__ FwdArgs a)
 {

@@ -12,16 +12,21 @@
 // row, the fewest whose lanes hold it.  In the backward pass a thread has the same columns
 // in every row of its team, so that dw and db are kept in its registers until the rows are
 // done; a CTA's teams join theirs in shared memory, and a second kernel joins the CTAs', both
-// in a fixed order.  The team follows from the width alone, so that a row's result does not
-// depend on the rows beside it.
+// in a fixed order.  The team follows from the width and from where the rows lie, so that a row's
+// result does not depend on the values beside it.  (Rows whose stride is off 16-byte boundaries are taken
+// in single elements; one row alone has no stride, and may be taken in vectors, in another order of sums.)
 //
 // Measured on a GB300 (graph replays, more inputs than L2 holds).  Forward: 8192 x 768 bf16 with fp32
 // weights 7.6 us (3.3 TB/s: three or four rows a team between its start and its end), 65536 x 768 33 us (6.1 TB/s),
-// 16384 x 1024 fp16 with residual 23.7 us (5.7 TB/s), 65536 x 4096 bf16 with residual 372 us (5.8).
+// 16384 x 1024 fp16 with residual 23.7 us (5.7 TB/s), fp32 without 21.9 (6.1), 65536 x 4096 bf16 with residual
+// 378 us (5.7).
 // Backward with the gradient past the norm: 8192 x 768 bf16 18.4 us (2.7 TB/s: 15 and 5 for the join,
 // cold), 65536 x 1024 89 us (6.0), 65536 x 4096 373 us (5.8); 16384 x 1024 fp32 39 us (5.2).
 // Rows in single elements: 20000 x 1001 fp16 22 us forward (3.6 TB/s), 45 backward (2.7), bound by the
 // instructions of an element at a time (35 and 58 with a team's size known only at run time).
+// Rows that no team holds, which a CTA goes over in passes: odd ones above 8192 values (8192 x 12001 bf16 with
+// residual 704 us, backward with ds 762; the floor is 116), any above 16384 (8192 x 20480 bf16 1052 and 1398; 198),
+// and forward fp32 ones with a residual above 8192 (4096 x 12288: 160; 119).
 #pragma once
 
 #include <algorithm>

@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(TW > kWarps ? 32 * TW : 32 * kWarps, TW > kWar
     sums.store(a.part, a.dim, reinterpret_cast<float*>(bytes), a.dim, me, step);
 }
 
-// fp32 rows of more than 8192 values, on 16-byte boundaries, whose ring would not fit: in registers, a CTA each.
+// fp32 rows of more than 8192 values, on 16-byte boundaries, whose ring would not fit: in registers, a CTA each, whose loads
+// have nothing beside them to hide behind (4096 x 12288 with ds 252 us, 3.2 TB/s).
 template <int K, bool DS> __global__ void __launch_bounds__(32 * kMaxTeam) norm_grad_wide_kernel(const __grid_constant__ BwdArgs a)
 {
     using P = Pack<DDP_F32, 4>;
@@ -301,7 +302,8 @@ template <int K, bool DS> __global__ void __launch_bounds__(32 * kMaxTeam) norm_
 }
 
 // Rows that no team holds: two passes over the row, which L2 keeps, in batches of columns whose loads are on their way
-// together.  The sums of a column, which belongs to one thread, are in the workspace.
+// together.  The sums of a column, which belongs to one thread, are in the workspace.  8192 x 12001 bf16 with ds 762 us
+// (1.0 TB/s): single elements, and each column's sums read and written for every row.
 constexpr int kBatch = 8;
 template <int DT> __global__ void __launch_bounds__(kLoopThreads) norm_grad_loop_kernel(const __grid_constant__ BwdArgs a)
 {
