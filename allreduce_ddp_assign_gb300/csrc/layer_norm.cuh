@@ -51,11 +51,6 @@ template <int DT, int N> struct __align__(N * sizeof(typename Elem<DT>::T)) Pack
     typename Elem<DT>::T v[N];
 };
 
-template <int DT, int N> __device__ __forceinline__ Pack<DT, N> load_pack(const void* p, int64_t i)
-{
-    return reinterpret_cast<const Pack<DT, N>*>(static_cast<const typename Elem<DT>::T*>(p))[i];
-}
-
 // A weight or bias: fp32 (wide) or in the rows' type, anywhere or on 16-byte boundaries (vectors).
 struct Columns {
     const void* p;
