@@ -1051,7 +1051,8 @@ ddp_status ddp_vocab_loss_backward(const void* hidden, int64_t hidden_stride, co
  *   weight, bias DEVICE w_dtype [dim]; bias NULL: none.  w_dtype is dtype or DDP_F32.
  *   mean, rstd   DEVICE float[ntokens].
  * Sums are fp32, the deviations taken around the mean.  A row with a NaN or an infinity
- * becomes NaN, and only it.  A row of equal values has rstd = 1 / sqrt(eps).  Rows that are
+ * becomes NaN, and only it.  A row of equal values has rstd = 1 / sqrt(eps), one whose
+ * squared deviations overflow fp32 in their sum (1e19 and more) rstd = 0.  Rows that are
  * strided or off 16-byte boundaries are read in 16-byte pieces: up to 14 bytes beside a row,
  * between the first row's begin and the last one's end, may be read and not used.  (The same
  * holds for the backward pass.)
@@ -1114,6 +1115,7 @@ typedef struct ddp_adamw_tensor {
  *   p <- p - lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
  * in fp32, p rounded once to param_dtype and once to copy_dtype.  A norm that is infinite
  * or NaN leaves everything as it is and does not count as a step.
+ * With eps 0 a value whose gradients have all been 0 becomes NaN (0 / 0).
  *
  * Blocks: tensor k has the blocks first_block[k] to first_block[k + 1] - 1, one for each
  * DDP_ADAMW_BLOCK of its values, the last one filled up with zeros.
